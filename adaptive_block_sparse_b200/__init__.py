@@ -5,7 +5,8 @@ kernels.  torch is used for device memory and streams.  Functions carry the C na
 
   nabla_reorder, nabla_build_mask, nabla_mask_lists, nabla_attn_fwd, nabla_attn_bwd,
   nabla_mask_workspace_bytes, nabla_fwd_workspace_bytes, nabla_bwd_workspace_bytes,
-  nabla_read_device_status, nabla_status_string.
+  nabla_read_device_status, nabla_status_string,
+  nabla_rotary, nabla_rotary_freqs, nabla_cache_append.
 
 The library is loaded on first use; a call raises ``ImportError`` if it has not been
 built (``python -m adaptive_block_sparse_b200.build``).  There is no fallback
@@ -43,7 +44,7 @@ EXPORTED = (
     "nabla_mask_lists", "nabla_fwd_workspace_bytes", "nabla_attn_fwd",
     "nabla_bwd_workspace_bytes", "nabla_attn_bwd", "nabla_read_device_status",
     "nabla_attn_fwd_noalloc", "nabla_attn_fwd_noalloc_status", "nabla_build_mask_sweep",
-    "nabla_selftest_bounded_wait",
+    "nabla_selftest_bounded_wait", "nabla_rotary_freqs", "nabla_rotary", "nabla_cache_append",
 )
 
 
@@ -53,6 +54,27 @@ class _Shape(ctypes.Structure):
 
 class _Window(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int32) for n in ("t", "h", "w")]
+
+
+class _Heads(ctypes.Structure):
+    _fields_ = [("ptr", ctypes.c_void_p), ("dtype", ctypes.c_int32), ("H", ctypes.c_int32),
+                ("stride_b", ctypes.c_int64), ("stride_h", ctypes.c_int64), ("stride_s", ctypes.c_int64)]
+
+
+class _Grid(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("T", "Hg", "W")]
+
+
+class _Rope(ctypes.Structure):
+    _fields_ = [("style", ctypes.c_int32), ("dim", ctypes.c_int32), ("axes", ctypes.c_int32),
+                ("axis_dim", ctypes.c_int32 * 3), ("magnitude", ctypes.c_float),
+                ("inv_freq", ctypes.c_void_p)]
+
+
+class _Cache(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("n_pages", ctypes.c_int32),
+                ("H", ctypes.c_int32), ("page", ctypes.c_int32), ("D", ctypes.c_int32),
+                ("dtype", ctypes.c_int32)]
 
 
 _vp = ctypes.c_void_p
@@ -82,6 +104,13 @@ _sigs = {
                                               ctypes.c_float, _vp, ctypes.c_int, _vp, ctypes.c_int,
                                               _vp]),
     "nabla_attn_fwd_noalloc_status": (ctypes.c_int, [ctypes.POINTER(ctypes.c_uint32), _vp]),
+    "nabla_rotary_freqs": (ctypes.c_int, [_i32, ctypes.c_double, ctypes.c_int, ctypes.c_double,
+                                          ctypes.c_double, _vp, ctypes.POINTER(ctypes.c_double)]),
+    "nabla_rotary": (ctypes.c_int, [_Heads, _Heads, _Heads, _Heads, _i32, _Grid, _i32, _Rope, _Grid, _vp,
+                                    ctypes.c_int, ctypes.c_int, _i32, _vp]),
+    "nabla_cache_append": (ctypes.c_int, [_Heads, _Heads, _Heads, _Heads, _i32, _i32, _Cache, _vp, _i32,
+                                          _vp, _vp, ctypes.POINTER(_Rope), _Grid, ctypes.c_int64, _vp,
+                                          _vp, _vp]),
 }
 
 
@@ -139,12 +168,15 @@ class Shape:
         return _Shape(self.B, self.H, self.T, self.Hg, self.W, self.D, self.P)
 
 
+_DTYPES = {torch.bfloat16: NABLA_BF16, torch.float32: NABLA_F32, torch.float16: NABLA_F16}
+
+
 def dtype_code(t) -> int:
     """nabla_dtype of a tensor (bf16, f32 or f16)."""
-    codes = {torch.bfloat16: NABLA_BF16, torch.float32: NABLA_F32, torch.float16: NABLA_F16}
-    if t.dtype not in codes:
+    code = _DTYPES.get(t.dtype)
+    if code is None:
         raise TypeError(f"unsupported dtype {t.dtype}")
-    return codes[t.dtype]
+    return code
 
 
 def _ptr(t):
@@ -343,6 +375,202 @@ def nabla_selftest_bounded_wait(workspace, stream=None):
 
 
 DEVICE_TIMEOUT_SELFTEST = 0x10A
+
+
+# ---------------------------------------------------------------------------------------
+# Continuing a clip from a history: rotary positions, paged cache
+# ---------------------------------------------------------------------------------------
+NABLA_ROPE_INTERLEAVED = 0
+NABLA_ROPE_HALF = 1
+NABLA_ROPE_PLAIN = 0
+NABLA_ROPE_LINEAR = 1
+NABLA_ROPE_BASE = 2
+NABLA_ROPE_PARTS = 3
+
+DEVICE_BAD_PAGE = 0x301
+DEVICE_BAD_LENGTH = 0x302
+
+_ABSENT = _Heads()
+
+
+def _heads(t, B, S, D, what):
+    """The [B, H, S, D] view of a tensor, strides included."""
+    if t.dim() != 4 or t.shape[0] != B or t.shape[2] != S or t.shape[3] != D:
+        raise ValueError(f"{what}: expected [{B}, H, {S}, {D}], got {tuple(t.shape)}")
+    sb, sh, ss, sd = t.stride()
+    if sd != 1:
+        raise ValueError(f"{what}: the last dimension must be contiguous")
+    return _Heads(t.data_ptr(), dtype_code(t), t.shape[1], sb, sh, ss)
+
+
+def _int_table(t, shape, what):
+    """Pointer of a contiguous int32 tensor of the given shape (None stays None)."""
+    if t is None:
+        return None
+    if t.dtype != torch.int32 or not t.is_contiguous() or tuple(t.shape) != shape:
+        raise ValueError(f"{what}: expected a contiguous int32 tensor {shape}, got {t.dtype} {tuple(t.shape)}")
+    return t.data_ptr()
+
+
+def _same_device(device, **tensors):
+    if device.type != "cuda":
+        raise ValueError(f"expected CUDA tensors, got {device}")
+    for name, t in tensors.items():
+        if t is not None and t.device != device:
+            raise ValueError(f"{name} is on {t.device}, the call on {device}")
+
+
+def _launch(device, stream, where, call):
+    """call(stream pointer) with the tensors' device current (a stream of that device)."""
+    if torch.cuda.current_device() == device.index:
+        rc = call((stream or torch.cuda.current_stream(device)).cuda_stream)
+    else:
+        with torch.cuda.device(device):
+            rc = call((stream or torch.cuda.current_stream(device)).cuda_stream)
+    if rc != NABLA_OK:
+        raise NablaError(rc, where)
+
+
+def _empty(shape, dtype, device, stream):
+    """Memory of the stream that will use it."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+class Rope:
+    """Rotary positions: frequencies, pairing and axes (see ``nabla_rope`` in nabla.h).
+
+    ``inv_freq``: fp64 CUDA tensor with one frequency per pair (radians per position).
+    ``axis_dims``: rotated channels of the (t, h, w) axes, or None for one axis.
+    """
+
+    __slots__ = ("inv_freq", "axes", "c")
+
+    def __init__(self, inv_freq, style=NABLA_ROPE_INTERLEAVED, axis_dims=None, magnitude=1.0):
+        if inv_freq.dtype != torch.float64 or inv_freq.dim() != 1 or not inv_freq.is_contiguous():
+            raise ValueError("inv_freq: expected a contiguous fp64 vector")
+        self.inv_freq = inv_freq
+        self.axes = 1 if axis_dims is None else 3
+        n = inv_freq.shape[0]
+        dims = (2 * n, 0, 0) if axis_dims is None else tuple(axis_dims)
+        self.c = _Rope(int(style), 2 * n, self.axes, dims, magnitude, inv_freq.data_ptr())
+
+    @classmethod
+    def build(cls, dim, device, style=NABLA_ROPE_INTERLEAVED, axis_dims=None, base=10000.0,
+              scaling=NABLA_ROPE_PLAIN, factor=1.0, trained_len=0.0):
+        """Frequencies base^(-2j/d) of one axis of ``dim`` channels or of three axes of
+        ``axis_dims`` channels each, scaled for longer contexts (``nabla_rotary_freqs``)."""
+        freqs, magnitude = [], 1.0
+        for d in (dim,) if axis_dims is None else axis_dims:
+            if d:
+                f, magnitude = nabla_rotary_freqs(d, base, scaling, factor, trained_len)
+                freqs += f
+        if 2 * len(freqs) != dim:
+            raise ValueError(f"axis_dims {axis_dims} do not add up to {dim}")
+        return cls(torch.tensor(freqs, dtype=torch.float64, device=device), style, axis_dims, magnitude)
+
+
+def nabla_rotary_freqs(dim, base=10000.0, scaling=NABLA_ROPE_PLAIN, factor=1.0, trained_len=0.0):
+    """(list of dim/2 frequencies of one axis, magnitude)."""
+    out = (ctypes.c_double * max(dim // 2, 1))()
+    mag = ctypes.c_double(1.0)
+    _check(load_library().nabla_rotary_freqs(int(dim), float(base), int(scaling), float(factor),
+                                             float(trained_len), ctypes.cast(out, _vp), ctypes.byref(mag)),
+           "nabla_rotary_freqs")
+    return list(out), mag.value
+
+
+def nabla_rotary(q, k, rope: Rope, grid=None, positions=None, origin=(0, 0, 0), q_out=None, k_out=None,
+                 out_dtype=None, src_layout=NABLA_LAYOUT_NATURAL, dst_layout=NABLA_LAYOUT_NATURAL,
+                 adjoint=False, stream=None):
+    """Rotary positions of ``q`` and ``k`` ([B, H, S, D] views; either may be None).
+
+    ``grid``: (T, Hg, W) of the latent, or None for a plain sequence.  ``positions``: int32
+    [B, S] or [B, S, axes] instead of the grid's.  ``adjoint`` maps the gradients of the
+    outputs to those of the inputs.  Returns (q_out, k_out), contiguous unless given.
+    """
+    x = q if q is not None else k
+    B, _, S, D = x.shape
+    device = x.device
+    _same_device(device, k=k, q_out=q_out, k_out=k_out, positions=positions, inv_freq=rope.inv_freq)
+    if grid is None:
+        grid = (S, 1, 1)
+    elif grid[0] * grid[1] * grid[2] != S:
+        raise ValueError(f"grid {tuple(grid)} does not hold {S} tokens")
+    views = []
+    outs = []
+    for t, o, what in ((q, q_out, "q"), (k, k_out, "k")):
+        if t is None:
+            if o is not None:
+                raise ValueError(f"{what}_out without {what}")
+            views += [_ABSENT, _ABSENT]
+        else:
+            if o is None:
+                o = _empty(t.shape, out_dtype or t.dtype, device, stream)
+            views += [_heads(t, B, S, D, what), _heads(o, B, S, D, what + "_out")]
+        outs.append(o)
+    pos = None
+    if positions is not None:
+        pos = _int_table(positions, (B, S) if positions.dim() == 2 and rope.axes == 1 else (B, S, rope.axes),
+                         "positions")
+    fn = load_library().nabla_rotary
+    _launch(device, stream, "nabla_rotary",
+            lambda st: fn(*views, B, _Grid(*grid), D, rope.c, _Grid(*origin), pos, int(src_layout),
+                          int(dst_layout), int(adjoint), st))
+    return outs[0], outs[1]
+
+
+def _cache(k_cache, v_cache):
+    if k_cache.dim() != 4 or k_cache.shape != v_cache.shape or k_cache.dtype != v_cache.dtype:
+        raise ValueError("k_cache and v_cache: expected two [pages, H, page, D] pools of one shape and dtype")
+    if not (k_cache.is_contiguous() and v_cache.is_contiguous()):
+        raise ValueError("k_cache and v_cache must be contiguous")
+    n, H, page, D = k_cache.shape
+    return _Cache(k_cache.data_ptr(), v_cache.data_ptr(), n, H, page, D, dtype_code(k_cache))
+
+
+def nabla_cache_append(k, v, k_cache, v_cache, page_table, start, rope: Rope = None, frame=(1, 1), pos0=0,
+                       positions=None, counts=None, q=None, q_out=None, status=None, stream=None):
+    """Append ``k`` (rotated on the way when ``rope`` is given) and ``v`` [B, H, S, D] to the
+    paged cache at the sequences' tokens start[b] .. start[b] + counts[b] - 1; with ``q``,
+    rotate it in the same launch.  ``frame``: (Hg, W) of a latent frame for three axes.
+    ``status``: uint8 or int32 CUDA tensor of at least 4 zeroed bytes for
+    ``nabla_read_device_status``.  Returns q_out (None without q)."""
+    B, _, S, D = k.shape
+    device = k.device
+    _same_device(device, v=v, k_cache=k_cache, v_cache=v_cache, page_table=page_table, start=start,
+                 positions=positions, counts=counts, q=q, q_out=q_out, status=status,
+                 inv_freq=rope.inv_freq if rope is not None else None)
+    cache = _cache(k_cache, v_cache)
+    qs = qd = _ABSENT
+    if q is not None:
+        if q_out is None:
+            q_out = _empty(q.shape, q.dtype, device, stream)
+        qs, qd = _heads(q, B, S, D, "q"), _heads(q_out, B, S, D, "q_out")
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    if D != k_cache.shape[3]:
+        raise ValueError(f"k has rows of {D}, the cache of {k_cache.shape[3]}")
+    if page_table.dim() != 2:
+        raise ValueError("page_table: expected [B, pages]")
+    width = page_table.shape[1]
+    pos = None
+    if positions is not None:
+        if rope is None:
+            raise ValueError("positions without rope")
+        pos = _int_table(positions, (B, S) if positions.dim() == 2 and rope.axes == 1 else (B, S, rope.axes),
+                         "positions")
+    if status is not None and status.numel() * status.element_size() < 4:
+        raise ValueError("status: expected at least 4 bytes")
+    args = (_heads(k, B, S, D, "k"), _heads(v, B, S, D, "v"), qs, qd, B, S, cache,
+            _int_table(page_table, (B, width), "page_table"), width, _int_table(start, (B,), "start"),
+            _int_table(counts, (B,), "counts"), ctypes.byref(rope.c) if rope is not None else None,
+            _Grid(0, *frame), int(pos0), pos, None if status is None else status.data_ptr())
+    fn = load_library().nabla_cache_append
+    _launch(device, stream, "nabla_cache_append", lambda st: fn(*args, st))
+    return q_out
 
 
 # ---------------------------------------------------------------------------------------

@@ -284,6 +284,121 @@ nabla_status nabla_selftest_bounded_wait(void *workspace, size_t workspace_bytes
 nabla_status nabla_read_device_status(void *workspace, uint32_t *code,
                                       nabla_stream_t stream);
 
+/* ---------------------------------------------------------------------------------
+ * Continuing a clip from a history (no counterpart in the NABLA pages)
+ * A long clip is generated in chunks of frames, often several candidates from one
+ * history.  The sparse attention above covers a chunk's own tokens; the calls below give
+ * Q and K their positions and keep the keys and values of finished frames in a paged
+ * cache.  Conventions differ from the calls above only as stated: any
+ * number of tokens, tensors as strided views, keys and values with fewer heads than the
+ * queries (grouped heads).
+ * --------------------------------------------------------------------------------- */
+
+/* A view [B, H, S, D] of D contiguous elements per row, strides in elements.  ptr and the
+ * strides of dimensions larger than 1 are multiples of 16 bytes; no stride is negative, and
+ * only sources may have a stride of 0 (broadcast).  ptr == NULL: absent. */
+typedef struct {
+  void *ptr;
+  int32_t dtype; /* nabla_dtype */
+  int32_t H;
+  int64_t stride_b, stride_h, stride_s;
+} nabla_heads;
+
+/* Latent frames x rows x columns (or an offset on that grid). */
+typedef struct {
+  int32_t T, Hg, W;
+} nabla_grid;
+
+/* Pairing of the rotated channels: (2i, 2i+1), or (i, i + dim/2). */
+typedef enum { NABLA_ROPE_INTERLEAVED = 0, NABLA_ROPE_HALF = 1 } nabla_rope_style;
+
+/* Rotary positions.  The leading `dim` channels of a head (even, 2..D) form dim/2 pairs;
+ * the rest is copied.  axes == 1: every pair turns with the token's one position.  axes ==
+ * 3: the first axis_dim[0]/2 pairs turn with the frame, the next axis_dim[1]/2 with the row,
+ * the last axis_dim[2]/2 with the column (axis_dim even, sum = dim).  Pair i turns by
+ * position * inv_freq[i] (DEVICE array of dim/2 fp64 values; angles are formed in fp64) and
+ * is multiplied by `magnitude` (1 unless a scaling asks for more). */
+typedef struct {
+  int32_t style; /* nabla_rope_style */
+  int32_t dim;
+  int32_t axes;
+  int32_t axis_dim[3];
+  float magnitude;
+  const double *inv_freq;
+} nabla_rope;
+
+/* Frequencies for contexts longer than the trained one (see nabla_rotary_freqs). */
+typedef enum {
+  NABLA_ROPE_PLAIN = 0,  /* base^(-2j/dim) */
+  NABLA_ROPE_LINEAR = 1, /* all divided by factor */
+  NABLA_ROPE_BASE = 2,   /* base raised by factor^(dim/(dim-2)) */
+  NABLA_ROPE_PARTS = 3   /* fast pairs kept, slow ones divided, a ramp between */
+} nabla_rope_scaling;
+
+/* Host helper: the dim/2 frequencies of one axis into the HOST array inv_freq, and the
+ * magnitude (nullable; 0.1 ln(factor) + 1 for PARTS, else 1).  PARTS keeps the pairs that
+ * turn 32 times or more within trained_len, divides those that turn once or less by factor
+ * and blends linearly between (trained_len is ignored otherwise).  base > 1, factor >= 1.
+ * Errors: INVALID_ARG. */
+nabla_status nabla_rotary_freqs(int32_t dim, double base, nabla_rope_scaling scaling, double factor,
+                                double trained_len, double *inv_freq, double *magnitude);
+
+/* Rotary positions of Q and K in one launch.
+ *   y0 = m (x0 cos a - x1 sin a),  y1 = m (x1 cos a + x0 sin a),  a = position * inv_freq
+ * q_src -> q_dst and k_src -> k_dst (either pair may be absent; both pairs share their source
+ *   and their destination dtype).  dtypes: bf16, fp16 or f32 on each side, not bf16 <-> fp16;
+ *   computed in f32, rounded once.  No destination may overlap a source.
+ * B, grid    : S = T * Hg * W tokens; token n is (t, h, w) with n = (t*Hg + h)*W + w.  A plain
+ *              sequence is T = S, Hg = W = 1.  B * S < 2^31.
+ * origin     : added to the positions taken from the grid (axes == 1: n + origin.T).
+ * positions  : nullable int32 [B, S, axes], natural token order; replaces grid and origin.
+ * src_layout,
+ * dst_layout : token order of the sources and destinations; the block order (REORDERED, as
+ *              nabla_reorder makes it) needs Hg and W in multiples of 8.
+ * adjoint    : 0, or 1 for the gradient: turns by -a (with the same magnitude), which is
+ *              the transpose of the forward map.
+ * Errors: INVALID_ARG, UNSUPPORTED (D not 64 or 128, sizes), CUDA. */
+nabla_status nabla_rotary(nabla_heads q_src, nabla_heads q_dst, nabla_heads k_src, nabla_heads k_dst,
+                          int32_t B, nabla_grid grid, int32_t D, nabla_rope rope, nabla_grid origin,
+                          const int32_t *positions, nabla_layout src_layout, nabla_layout dst_layout,
+                          int32_t adjoint, nabla_stream_t stream);
+
+/* A paged cache of keys and values: two pools [n_pages, H, page, D] of bf16 or fp16.  page:
+ * tokens per page, a power of two from 16 to 4096.  A sequence is a list of page numbers; its
+ * token i is slot i % page of its page i / page.  Page numbers outside [0, n_pages) are never
+ * dereferenced: they are reported (0x301), as are lengths below 0 or beyond a page list
+ * (0x302). */
+typedef struct {
+  void *k, *v;
+  int32_t n_pages, H, page, D;
+  int32_t dtype; /* nabla_dtype */
+} nabla_cache;
+
+/* Appends S new tokens of each of B sequences to the cache, K rotated on the way, and
+ * optionally rotates Q in the same launch.
+ * k, v       : [B, cache.H, S, D], the cache's dtype.
+ * q_src,
+ * q_dst      : optional (both ptr NULL), any number of heads, same dtype; all S tokens are
+ *              rotated, those beyond counts too.  Needs rope.
+ * page_table : int32 [B, table_width] page numbers; table_width * page < 2^31.
+ * start      : int32 [B], index in its sequence of each sequence's first new token.
+ * counts     : nullable int32 [B]: tokens to append of each sequence (the first counts[b] of
+ *              its S; NULL = all S).  The others write nothing.
+ * rope       : nullable (host pointer): without it K is stored as given.  The position of a
+ *              token is p = pos0 + its index in the sequence; with three axes p = (t, h, w)
+ *              on frames of frame.Hg x frame.W tokens (frame.T is ignored).
+ * positions  : nullable int32 [B, S, axes], replaces p.
+ * status     : nullable device word that receives 0x301 / 0x302 (first one wins; the token
+ *              concerned is skipped).  The call does not clear it: zero it before its
+ *              first use; nabla_read_device_status reads and clears it.
+ * Two tokens of one call must not land in the same slot.  Errors: INVALID_ARG, UNSUPPORTED,
+ * CUDA. */
+nabla_status nabla_cache_append(nabla_heads k, nabla_heads v, nabla_heads q_src, nabla_heads q_dst,
+                                int32_t B, int32_t S, nabla_cache cache, const int32_t *page_table,
+                                int32_t table_width, const int32_t *start, const int32_t *counts,
+                                const nabla_rope *rope, nabla_grid frame, int64_t pos0,
+                                const int32_t *positions, uint32_t *status, nabla_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

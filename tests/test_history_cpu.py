@@ -1,0 +1,156 @@
+"""Rotary positions and the paged cache on the host: the oracle against closed forms, the
+frequencies, and the C entry points' refusals (nothing reaches a GPU)."""
+import ctypes
+import math
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import history as H
+
+
+@pytest.fixture(scope="module")
+def nb():
+    from adaptive_block_sparse_b200 import build as b
+    b.build()
+    import adaptive_block_sparse_b200 as m
+    m.load_library()
+    return m
+
+
+def test_oracle_rotary_is_a_rotation():
+    rng = np.random.default_rng(0)
+    x = rng.normal(size=(1, 2, 5, 64))
+    f, _ = H.rotary_freqs(64)
+    pos = H.grid_positions(5, 1, 1, 1, first=9)[None]
+    for inter in (True, False):
+        y = H.rotary(x, pos, f, inter)
+        np.testing.assert_allclose((y ** 2).sum(-1), (x ** 2).sum(-1), rtol=1e-12)
+        np.testing.assert_allclose(H.rotary(y, pos, f, inter, adjoint=True), x, atol=1e-12)
+        # logits depend on the distance of positions alone
+        a = H.rotary(x[:, :, :1], pos[:, :1], f, inter)[0, 0, 0] @ H.rotary(x[:, 1:, 1:2], pos[:, :1] + 3, f, inter)[0, 0, 0]
+        b = H.rotary(x[:, :, :1], pos[:, :1] + 50, f, inter)[0, 0, 0] @ H.rotary(x[:, 1:, 1:2], pos[:, :1] + 53, f, inter)[0, 0, 0]
+        assert abs(a - b) < 1e-10
+    # one pair, a quarter turn
+    y = H.rotary(np.array([[[[3.0, 4.0]]]]), np.array([[[1]]]), np.array([math.pi / 2]), True)
+    np.testing.assert_allclose(y, [[[[-4.0, 3.0]]]], atol=1e-12)
+
+
+def test_oracle_append_and_positions():
+    assert H.grid_positions(3, 4, 5, 3, first=19).tolist() == [[0, 3, 4], [1, 0, 0], [1, 0, 1]]
+    c = H.append(np.zeros((3, 1, 2, 1)), np.arange(1.0, 4.0).reshape(1, 1, 3, 1), [[2, 0]], [1], [3])
+    assert c.reshape(3, 2).tolist() == [[2, 3], [0, 0], [0, 1]]
+
+
+@pytest.mark.parametrize("scaling", ["plain", "linear", "base", "parts"])
+@pytest.mark.parametrize("dim", [2, 4, 42, 44, 64, 96, 128])
+def test_frequencies(nb, scaling, dim):
+    code = {"plain": nb.NABLA_ROPE_PLAIN, "linear": nb.NABLA_ROPE_LINEAR, "base": nb.NABLA_ROPE_BASE,
+            "parts": nb.NABLA_ROPE_PARTS}[scaling]
+    got, mag = nb.nabla_rotary_freqs(dim, 10000.0, code, 8.0, 4096)
+    want, wmag = H.rotary_freqs(dim, 10000.0, scaling, 8.0, 4096)
+    np.testing.assert_allclose(got, want, rtol=1e-13)
+    assert mag == pytest.approx(wmag, rel=1e-15)
+    assert got[0] == (0.125 if scaling == "linear" else 1.0)
+    # the slowest pair ends divided by the factor (base: by design at the last pair)
+    if scaling in ("base", "parts", "linear") and dim >= 42:
+        assert got[-1] == pytest.approx(10000.0 ** (-(dim - 2) / dim) / 8, rel=1e-12)
+
+
+def test_frequencies_refuse(nb):
+    bad = [dict(dim=3), dict(dim=0), dict(base=1.0), dict(base=math.nan), dict(factor=0.5), dict(scaling=4),
+           dict(scaling=-1), dict(scaling=nb.NABLA_ROPE_PARTS, trained_len=0.0)]
+    for kw in bad:
+        with pytest.raises(nb.NablaError) as e:
+            nb.nabla_rotary_freqs(**{"dim": 64, **kw})
+        assert e.value.status == nb.NABLA_ERR_INVALID_ARG
+
+
+A, B2, C3, D4 = 0x10000000, 0x20000000, 0x30000000, 0x40000000    # fake, aligned, never dereferenced
+
+
+def _view(nb, ptr, Hh=2, dtype=0, S=32, D=64, **kw):
+    d = dict(ptr=ptr, dtype=dtype, H=Hh, stride_b=Hh * S * D, stride_h=S * D, stride_s=D)
+    d.update(kw)
+    return nb._Heads(*[d[k] for k in ("ptr", "dtype", "H", "stride_b", "stride_h", "stride_s")])
+
+
+def _rope(nb, style=0, dim=64, axes=1, dims=(64, 0, 0), mag=1.0, freq=0x5000):
+    return nb._Rope(style, dim, axes, dims, mag, freq)
+
+
+def test_rotary_refuses(nb):
+    lib = nb.load_library()
+    INV, UNS = nb.NABLA_ERR_INVALID_ARG, nb.NABLA_ERR_UNSUPPORTED
+
+    def call(qs=None, qd=None, ks=nb._Heads(), kd=nb._Heads(), B=1, grid=(2, 16, 1), D=64, rope=None,
+             pos=None, sl=1, dl=1, adj=0):
+        return lib.nabla_rotary(qs or _view(nb, A), qd or _view(nb, B2), ks, kd, B, nb._Grid(*grid), D,
+                                rope or _rope(nb), nb._Grid(0, 0, 0), pos, sl, dl, adj, None)
+    assert call(B=0) == INV and call(grid=(0, 1, 1)) == INV and call(D=96) == UNS
+    assert call(rope=_rope(nb, style=2)) == INV and call(rope=_rope(nb, dim=66)) == INV
+    assert call(rope=_rope(nb, dim=7)) == INV and call(rope=_rope(nb, dim=0)) == INV
+    assert call(rope=_rope(nb, axes=2)) == INV and call(rope=_rope(nb, axes=3, dims=(20, 20, 20))) == INV
+    assert call(rope=_rope(nb, axes=3, dims=(21, 21, 22))) == INV
+    assert call(rope=_rope(nb, freq=None)) == INV and call(rope=_rope(nb, freq=0x5004)) == INV
+    assert call(rope=_rope(nb, mag=math.nan)) == INV
+    assert call(adj=2) == INV and call(sl=2) == INV and call(dl=-1) == INV
+    assert call(dl=0) == INV                                           # 16 x 1 is no grid of 8 x 8 patches
+    assert call(grid=(1 << 20, 1 << 12, 1)) == UNS                     # 2^32 tokens
+    assert call(pos=0x10002) == INV
+    assert call(qs=nb._Heads(), qd=nb._Heads()) == INV                 # nothing to do
+    assert call(qd=nb._Heads()) == INV and call(qs=_view(nb, A + 8)) == INV
+    assert call(qs=_view(nb, A, stride_s=68)) == INV                   # rows not 16-byte aligned
+    assert call(qs=_view(nb, A, stride_s=-64)) == INV
+    assert call(qd=_view(nb, B2, stride_h=0)) == INV                   # a destination written twice
+    assert call(qd=_view(nb, B2, Hh=3)) == INV and call(qs=_view(nb, A, Hh=0)) == INV
+    assert call(qs=_view(nb, A, dtype=7)) == INV and call(qd=_view(nb, B2, dtype=2)) == INV   # bf16 -> fp16
+    assert call(qd=_view(nb, A)) == INV                                # in place
+    assert call(qd=_view(nb, A + 64 * 64)) == INV                      # overlap
+    assert call(ks=_view(nb, C3, dtype=1), kd=_view(nb, D4)) == INV    # Q and K of different dtypes
+    assert call(ks=_view(nb, C3), kd=_view(nb, A)) == INV              # K's output over Q's input
+
+
+def test_append_refuses(nb):
+    lib = nb.load_library()
+    INV, UNS = nb.NABLA_ERR_INVALID_ARG, nb.NABLA_ERR_UNSUPPORTED
+
+    def cache(k=C3, v=D4, n=4, Hh=2, page=16, D=64, dtype=0):
+        return nb._Cache(k, v, n, Hh, page, D, dtype)
+
+    def call(k=None, v=None, qs=nb._Heads(), qd=nb._Heads(), B=1, S=32, c=None, table=0x1000, width=4,
+             start=0x2000, counts=None, rope=None, frame=(0, 1, 1), pos0=0, pos=None, status=None):
+        return lib.nabla_cache_append(k or _view(nb, A), v or _view(nb, B2), qs, qd, B, S, c or cache(), table,
+                                      width, start, counts, ctypes.byref(rope) if rope else None,
+                                      nb._Grid(*frame), pos0, pos, status, None)
+    assert call(B=0) == INV and call(S=0) == INV
+    assert call(c=cache(page=24)) == UNS and call(c=cache(page=8)) == UNS and call(c=cache(page=8192)) == UNS
+    assert call(c=cache(D=96)) == UNS and call(c=cache(n=0)) == INV and call(c=cache(dtype=1)) == INV
+    assert call(c=cache(k=None)) == INV and call(c=cache(v=D4 + 8)) == INV
+    assert call(c=cache(v=C3)) == INV                                  # one pool over the other
+    assert call(table=None) == INV and call(width=0) == INV and call(start=None) == INV
+    assert call(table=0x1002) == INV and call(counts=0x1001) == INV and call(status=0x1002) == INV
+    assert call(c=cache(page=4096), width=1 << 20) == UNS
+    assert call(pos0=-1) == INV
+    assert call(k=_view(nb, A, Hh=3)) == INV and call(v=_view(nb, B2, dtype=2)) == INV
+    assert call(k=_view(nb, C3)) == INV                                # a source inside the pool
+    assert call(rope=_rope(nb, dim=68)) == INV
+    assert call(rope=_rope(nb, axes=3, dims=(20, 20, 24)), frame=(0, 0, 4)) == INV
+    q = _view(nb, 0x50000000, Hh=4)
+    qd = _view(nb, 0x60000000, Hh=4)
+    assert call(qs=q, qd=qd) == INV                                    # Q without a rope
+    assert call(qs=q, qd=q, rope=_rope(nb)) == INV                     # in place
+    assert call(qs=q, qd=_view(nb, A, Hh=4), rope=_rope(nb)) == INV    # over K
+    assert call(qs=q, rope=_rope(nb)) == INV
+
+
+def test_binding_refuses(nb):
+    x = torch.zeros(1, 2, 4, 64)
+    freq = torch.ones(32, dtype=torch.float64)
+    with pytest.raises(ValueError):
+        nb.Rope(freq.float())
+    with pytest.raises(ValueError):
+        nb.Rope.build(64, "cpu", axis_dims=(20, 20, 20))
+    with pytest.raises(ValueError):
+        nb.nabla_rotary(x, None, nb.Rope(freq))                        # not on a GPU
