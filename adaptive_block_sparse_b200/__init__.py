@@ -67,7 +67,8 @@ class _Grid(ctypes.Structure):
 
 class _Rope(ctypes.Structure):
     _fields_ = [("style", ctypes.c_int32), ("dim", ctypes.c_int32), ("axes", ctypes.c_int32),
-                ("axis_dim", ctypes.c_int32 * 3), ("magnitude", ctypes.c_float),
+                ("dim_t", ctypes.c_int32), ("dim_h", ctypes.c_int32), ("dim_w", ctypes.c_int32),
+                ("magnitude", ctypes.c_float),
                 ("inv_freq", ctypes.c_void_p)]
 
 
@@ -395,48 +396,51 @@ _ABSENT = _Heads()
 
 def _heads(t, B, S, D, what):
     """The [B, H, S, D] view of a tensor, strides included."""
-    if t.dim() != 4 or t.shape[0] != B or t.shape[2] != S or t.shape[3] != D:
-        raise ValueError(f"{what}: expected [{B}, H, {S}, {D}], got {tuple(t.shape)}")
+    shape = t.shape
+    if len(shape) != 4 or shape[0] != B or shape[2] != S or shape[3] != D:
+        raise ValueError(f"{what}: expected [{B}, H, {S}, {D}], got {tuple(shape)}")
     sb, sh, ss, sd = t.stride()
     if sd != 1:
         raise ValueError(f"{what}: the last dimension must be contiguous")
-    return _Heads(t.data_ptr(), dtype_code(t), t.shape[1], sb, sh, ss)
+    return _Heads(t.data_ptr(), dtype_code(t), shape[1], sb, sh, ss)
 
 
 def _int_table(t, shape, what):
     """Pointer of a contiguous int32 tensor of the given shape (None stays None)."""
     if t is None:
         return None
-    if t.dtype != torch.int32 or not t.is_contiguous() or tuple(t.shape) != shape:
+    if t.dtype is not torch.int32 or t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{what}: expected a contiguous int32 tensor {shape}, got {t.dtype} {tuple(t.shape)}")
     return t.data_ptr()
 
 
-def _same_device(device, **tensors):
+def _same_device(device, tensors, names):
     if device.type != "cuda":
         raise ValueError(f"expected CUDA tensors, got {device}")
-    for name, t in tensors.items():
+    for i, t in enumerate(tensors):
         if t is not None and t.device != device:
-            raise ValueError(f"{name} is on {t.device}, the call on {device}")
+            raise ValueError(f"{names.split()[i]} is on {t.device}, the call on {device}")
 
 
-def _launch(device, stream, where, call):
-    """call(stream pointer) with the tensors' device current (a stream of that device)."""
-    if torch.cuda.current_device() == device.index:
-        rc = call((stream or torch.cuda.current_stream(device)).cuda_stream)
+def _launch(device, stream, where, fn, *args):
+    """fn(*args, stream pointer) with the tensors' device current (a stream of that device)."""
+    index = device.index
+    st = torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
+    if torch.cuda.current_device() == index:
+        rc = fn(*args, st)
     else:
         with torch.cuda.device(device):
-            rc = call((stream or torch.cuda.current_stream(device)).cuda_stream)
+            rc = fn(*args, st)
     if rc != NABLA_OK:
         raise NablaError(rc, where)
 
 
-def _empty(shape, dtype, device, stream):
-    """Memory of the stream that will use it."""
+def _empty_like(t, dtype, stream):
+    """Contiguous memory of t's shape, owned by the stream that will use it."""
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
+        return torch.empty_like(t, dtype=dtype, memory_format=torch.contiguous_format)
     with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=device)
+        return torch.empty_like(t, dtype=dtype, memory_format=torch.contiguous_format)
 
 
 class Rope:
@@ -449,13 +453,13 @@ class Rope:
     __slots__ = ("inv_freq", "axes", "c")
 
     def __init__(self, inv_freq, style=NABLA_ROPE_INTERLEAVED, axis_dims=None, magnitude=1.0):
-        if inv_freq.dtype != torch.float64 or inv_freq.dim() != 1 or not inv_freq.is_contiguous():
+        if inv_freq.dtype is not torch.float64 or inv_freq.dim() != 1 or not inv_freq.is_contiguous():
             raise ValueError("inv_freq: expected a contiguous fp64 vector")
         self.inv_freq = inv_freq
         self.axes = 1 if axis_dims is None else 3
-        n = inv_freq.shape[0]
-        dims = (2 * n, 0, 0) if axis_dims is None else tuple(axis_dims)
-        self.c = _Rope(int(style), 2 * n, self.axes, dims, magnitude, inv_freq.data_ptr())
+        dim = 2 * inv_freq.shape[0]
+        t, h, w = (dim, 0, 0) if axis_dims is None else axis_dims
+        self.c = _Rope(style, dim, self.axes, t, h, w, magnitude, inv_freq.data_ptr())
 
     @classmethod
     def build(cls, dim, device, style=NABLA_ROPE_INTERLEAVED, axis_dims=None, base=10000.0,
@@ -494,32 +498,31 @@ def nabla_rotary(q, k, rope: Rope, grid=None, positions=None, origin=(0, 0, 0), 
     x = q if q is not None else k
     B, _, S, D = x.shape
     device = x.device
-    _same_device(device, k=k, q_out=q_out, k_out=k_out, positions=positions, inv_freq=rope.inv_freq)
+    _same_device(device, (k, q_out, k_out, positions, rope.inv_freq), "k q_out k_out positions inv_freq")
     if grid is None:
         grid = (S, 1, 1)
     elif grid[0] * grid[1] * grid[2] != S:
         raise ValueError(f"grid {tuple(grid)} does not hold {S} tokens")
-    views = []
-    outs = []
-    for t, o, what in ((q, q_out, "q"), (k, k_out, "k")):
-        if t is None:
-            if o is not None:
-                raise ValueError(f"{what}_out without {what}")
-            views += [_ABSENT, _ABSENT]
-        else:
-            if o is None:
-                o = _empty(t.shape, out_dtype or t.dtype, device, stream)
-            views += [_heads(t, B, S, D, what), _heads(o, B, S, D, what + "_out")]
-        outs.append(o)
+    qs = qd = ks = kd = _ABSENT
+    if q is not None:
+        if q_out is None:
+            q_out = _empty_like(q, out_dtype, stream)
+        qs, qd = _heads(q, B, S, D, "q"), _heads(q_out, B, S, D, "q_out")
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    if k is not None:
+        if k_out is None:
+            k_out = _empty_like(k, out_dtype, stream)
+        ks, kd = _heads(k, B, S, D, "k"), _heads(k_out, B, S, D, "k_out")
+    elif k_out is not None:
+        raise ValueError("k_out without k")
     pos = None
     if positions is not None:
         pos = _int_table(positions, (B, S) if positions.dim() == 2 and rope.axes == 1 else (B, S, rope.axes),
                          "positions")
-    fn = load_library().nabla_rotary
-    _launch(device, stream, "nabla_rotary",
-            lambda st: fn(*views, B, _Grid(*grid), D, rope.c, _Grid(*origin), pos, int(src_layout),
-                          int(dst_layout), int(adjoint), st))
-    return outs[0], outs[1]
+    _launch(device, stream, "nabla_rotary", load_library().nabla_rotary, qs, qd, ks, kd, B, _Grid(*grid), D,
+            rope.c, _Grid(*origin), pos, src_layout, dst_layout, int(adjoint))
+    return q_out, k_out
 
 
 def _cache(k_cache, v_cache):
@@ -540,14 +543,14 @@ def nabla_cache_append(k, v, k_cache, v_cache, page_table, start, rope: Rope = N
     ``nabla_read_device_status``.  Returns q_out (None without q)."""
     B, _, S, D = k.shape
     device = k.device
-    _same_device(device, v=v, k_cache=k_cache, v_cache=v_cache, page_table=page_table, start=start,
-                 positions=positions, counts=counts, q=q, q_out=q_out, status=status,
-                 inv_freq=rope.inv_freq if rope is not None else None)
+    _same_device(device, (v, k_cache, v_cache, page_table, start, positions, counts, q, q_out, status,
+                          rope.inv_freq if rope is not None else None),
+                 "v k_cache v_cache page_table start positions counts q q_out status inv_freq")
     cache = _cache(k_cache, v_cache)
     qs = qd = _ABSENT
     if q is not None:
         if q_out is None:
-            q_out = _empty(q.shape, q.dtype, device, stream)
+            q_out = _empty_like(q, None, stream)
         qs, qd = _heads(q, B, S, D, "q"), _heads(q_out, B, S, D, "q_out")
     elif q_out is not None:
         raise ValueError("q_out without q")
@@ -564,12 +567,11 @@ def nabla_cache_append(k, v, k_cache, v_cache, page_table, start, rope: Rope = N
                          "positions")
     if status is not None and status.numel() * status.element_size() < 4:
         raise ValueError("status: expected at least 4 bytes")
-    args = (_heads(k, B, S, D, "k"), _heads(v, B, S, D, "v"), qs, qd, B, S, cache,
+    _launch(device, stream, "nabla_cache_append", load_library().nabla_cache_append,
+            _heads(k, B, S, D, "k"), _heads(v, B, S, D, "v"), qs, qd, B, S, cache,
             _int_table(page_table, (B, width), "page_table"), width, _int_table(start, (B,), "start"),
             _int_table(counts, (B,), "counts"), ctypes.byref(rope.c) if rope is not None else None,
-            _Grid(0, *frame), int(pos0), pos, None if status is None else status.data_ptr())
-    fn = load_library().nabla_cache_append
-    _launch(device, stream, "nabla_cache_append", lambda st: fn(*args, st))
+            _Grid(0, *frame), pos0, pos, None if status is None else status.data_ptr())
     return q_out
 
 

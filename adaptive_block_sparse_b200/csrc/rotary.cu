@@ -25,7 +25,7 @@
 namespace nabla {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
 enum { kInterleaved = 0, kHalf = 1, kHalfOdd = 2 };   // pairing; kHalfOdd: dim / 2 % 8 != 0
 
 // One tensor to move: source and destination views (strides in elements).
@@ -217,7 +217,7 @@ __device__ __forceinline__ void angle(const RotaryParams& p, const Token& k, int
 template <int PAIRING, int D, typename TS, typename TD>
 __global__ void __launch_bounds__(kThreads) rotary_kernel(const __grid_constant__ RotaryParams p) {
   constexpr int kLanes = PAIRING == kHalfOdd ? D / 8 : D / 16;          // threads per token
-  constexpr int kUnroll = PAIRING == kHalfOdd ? 2 : (sizeof(TS) == 4 ? 2 : 4);
+  constexpr int kUnroll = 2;
   const long long gid = static_cast<long long>(blockIdx.x) * kThreads + threadIdx.x;
   const long long token = gid / kLanes;
   if (token >= p.tokens) return;
@@ -354,9 +354,12 @@ template <int PAIRING, int D, typename TS, typename TD>
 cudaError_t go(RotaryParams p, cudaStream_t st) {
   constexpr int kLanes = PAIRING == kHalfOdd ? D / 8 : D / 16;
   const long long lanes = static_cast<long long>(p.tokens) * kLanes;
-  // Heads per thread: as many as leave about eight blocks' worth of threads a slot of the
-  // GPU (148 SMs x 1024 threads); a small call spreads its heads over threads instead.
-  long long g = lanes * p.heads / (148LL * 1024 * 8);
+  // Heads per thread: as many as leave about 5 warps of threads on each of the GPU's 592
+  // schedulers, so that the angles (about 3 us of latency) are shared by many heads; a small
+  // call spreads its heads over threads instead.  Sequences [3, 4097] of 24 heads: 118 us at
+  // one head a thread, 33 us at four and more; blocks of 128 threads and two heads in flight
+  // beat 256 and four (720p-like Q and K 499 against 507 us).
+  long long g = lanes * p.heads / (148LL * 768);
   g = g < 1 ? 1 : (g > p.heads ? p.heads : g);
   const int groups = static_cast<int>((p.heads + g - 1) / g);
   p.group = (p.heads + groups - 1) / groups;

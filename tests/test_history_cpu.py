@@ -77,7 +77,7 @@ def _view(nb, ptr, Hh=2, dtype=0, S=32, D=64, **kw):
 
 
 def _rope(nb, style=0, dim=64, axes=1, dims=(64, 0, 0), mag=1.0, freq=0x5000):
-    return nb._Rope(style, dim, axes, dims, mag, freq)
+    return nb._Rope(style, dim, axes, *dims, mag, freq)
 
 
 def test_rotary_refuses(nb):
