@@ -6,7 +6,8 @@ kernels.  torch is used for device memory and streams.  Functions carry the C na
   nabla_reorder, nabla_build_mask, nabla_mask_lists, nabla_attn_fwd, nabla_attn_bwd,
   nabla_mask_workspace_bytes, nabla_fwd_workspace_bytes, nabla_bwd_workspace_bytes,
   nabla_read_device_status, nabla_status_string,
-  nabla_rotary, nabla_rotary_freqs, nabla_cache_append.
+  nabla_rotary, nabla_rotary_freqs, nabla_cache_append, nabla_prefix_attn,
+  nabla_prefix_workspace_bytes.
 
 The library is loaded on first use; a call raises ``ImportError`` if it has not been
 built (``python -m adaptive_block_sparse_b200.build``).  There is no fallback
@@ -45,6 +46,7 @@ EXPORTED = (
     "nabla_bwd_workspace_bytes", "nabla_attn_bwd", "nabla_read_device_status",
     "nabla_attn_fwd_noalloc", "nabla_attn_fwd_noalloc_status", "nabla_build_mask_sweep",
     "nabla_selftest_bounded_wait", "nabla_rotary_freqs", "nabla_rotary", "nabla_cache_append",
+    "nabla_prefix_workspace_bytes", "nabla_prefix_attn",
 )
 
 
@@ -112,6 +114,9 @@ _sigs = {
     "nabla_cache_append": (ctypes.c_int, [_Heads, _Heads, _Heads, _Heads, _i32, _i32, _Cache, _vp, _i32,
                                           _vp, _vp, ctypes.POINTER(_Rope), _Grid, ctypes.c_int64, _vp,
                                           _vp, _vp]),
+    "nabla_prefix_workspace_bytes": (_sz, [_i32, _i32, _i32, _i32, _i32]),
+    "nabla_prefix_attn": (ctypes.c_int, [_Heads, _i32, _i32, _Cache, _vp, _i32, _vp, _i32, _vp, _vp, _i32,
+                                         ctypes.c_float, _Heads, _vp, _Heads, _vp, _vp, _sz, _vp]),
 }
 
 
@@ -573,6 +578,67 @@ def nabla_cache_append(k, v, k_cache, v_cache, page_table, start, rope: Rope = N
             _int_table(counts, (B,), "counts"), ctypes.byref(rope.c) if rope is not None else None,
             _Grid(0, *frame), pos0, pos, None if status is None else status.data_ptr())
     return q_out
+
+
+def nabla_prefix_workspace_bytes(B, Hq, Hkv, Sq, D) -> int:
+    return int(load_library().nabla_prefix_workspace_bytes(B, Hq, Hkv, Sq, D))
+
+
+def _f32_rows(t, B, H, S, what):
+    """Pointer of a contiguous f32 [B, H, S] tensor (None stays None)."""
+    if t is None:
+        return None
+    if t.dtype is not torch.float32 or t.shape != (B, H, S) or not t.is_contiguous():
+        raise ValueError(f"{what}: expected a contiguous f32 tensor {(B, H, S)}, got {t.dtype} {tuple(t.shape)}")
+    return t.data_ptr()
+
+
+def nabla_prefix_attn(q, k_cache, v_cache, prefix_pages, prefix_len, tail_pages=None, tail_len=None, q_len=None,
+                      causal=False, scale=None, part_o=None, part_lse=None, o=None, o_dtype=None, lse=None,
+                      workspace=None, stream=None):
+    """Attention of ``q`` [B, Hq, Sq, D] over a shared prefix of ``prefix_len`` tokens in the
+    pages ``prefix_pages`` and each sequence's own ``tail_len[b]`` tokens in the pages
+    ``tail_pages[b]``; ``part_o`` / ``part_lse`` merge a result over other keys (the
+    block-sparse forward's O and LSE).  Returns (o, lse); ``lse`` is written when given.  The
+    first word of ``workspace`` receives the device status (``nabla_read_device_status``)."""
+    B, Hq, Sq, D = q.shape
+    device = q.device
+    _same_device(device, (k_cache, v_cache, prefix_pages, tail_pages, tail_len, q_len, part_o, part_lse, o, lse,
+                          workspace),
+                 "k_cache v_cache prefix_pages tail_pages tail_len q_len part_o part_lse o lse workspace")
+    cache = _cache(k_cache, v_cache)
+    if cache.D != D:
+        raise ValueError(f"q has rows of {D}, the cache of {cache.D}")
+    if o is None:
+        o = _empty_like(q, o_dtype, stream)
+    lib = load_library()
+    if workspace is None:
+        need = lib.nabla_prefix_workspace_bytes(B, Hq, cache.H, Sq, D)
+        if stream is None:
+            workspace = torch.empty(need, dtype=torch.uint8, device=device)
+        else:
+            with torch.cuda.stream(stream):
+                workspace = torch.empty(need, dtype=torch.uint8, device=device)
+    elif workspace.dtype is not torch.uint8 or not workspace.is_contiguous():
+        raise ValueError("workspace: expected a contiguous uint8 tensor")
+    n_prefix = 0
+    if prefix_pages is not None:
+        n_prefix = prefix_pages.shape[0]
+        if n_prefix * cache.page < prefix_len:
+            raise ValueError(f"{n_prefix} pages of {cache.page} do not hold a prefix of {prefix_len}")
+    width = 0
+    if tail_pages is not None:
+        if tail_pages.dim() != 2:
+            raise ValueError("tail_pages: expected [B, pages]")
+        width = tail_pages.shape[1]
+    _launch(device, stream, "nabla_prefix_attn", lib.nabla_prefix_attn, _heads(q, B, Sq, D, "q"), B, Sq, cache,
+            _int_table(prefix_pages, (n_prefix,), "prefix_pages"), prefix_len,
+            _int_table(tail_pages, (B, width), "tail_pages"), width, _int_table(tail_len, (B,), "tail_len"),
+            _int_table(q_len, (B,), "q_len"), int(causal), 1.0 / math.sqrt(D) if scale is None else scale,
+            _ABSENT if part_o is None else _heads(part_o, B, Sq, D, "part_o"),
+            _f32_rows(part_lse, B, Hq, Sq, "part_lse"), _heads(o, B, Sq, D, "o"),
+            _f32_rows(lse, B, Hq, Sq, "lse"), workspace.data_ptr(), workspace.numel())
+    return o, lse
 
 
 # ---------------------------------------------------------------------------------------

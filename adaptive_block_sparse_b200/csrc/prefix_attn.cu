@@ -1,0 +1,1116 @@
+// Attention of a batch over one shared prefix and each sequence's own tail, keys and values
+// in a paged cache (sm_100a).
+//
+// The softmax runs in one pass over the keys: a row keeps a reference maximum m and the sum
+// l of 2^(s - m), and its accumulator O = sum 2^(s - m) v is rescaled only when the maximum
+// grows by more than 2^8.  Results over disjoint sets of keys are joined by their log-sums:
+// LSE = log2(2^a + 2^b), O = 2^(a - LSE) Oa + 2^(b - LSE) Ob.
+//
+// Work.  An item is a tile of up to 256 query rows of one key head and a run of 128-key
+// tiles.  The heads that share a key head are rows too (row = query * G + head in group), so
+// a key tile is read once for all of them.
+//   * own mode (a sequence has at least 256 rows per key head): an item is 256 rows of one
+//     sequence and walks the prefix, then the sequence's tail;
+//   * shared mode (fewer rows): the rows of ALL sequences are tiled together for the
+//     prefix, so its keys and values leave HBM once for the batch; each sequence's tail is
+//     one more item, and every result is a part that the combine kernel joins.
+// The unit of scheduling is one key tile.  A CTA (one per SM) first takes whole items, one
+// per round while all CTAs have one (own mode); what is left over is cut into equal runs of
+// units, wherever they fall inside items, so no SM waits for a long item.  Item lengths
+// follow from the device's tail lengths: every CTA sums the units and finds its run
+// itself, so a captured launch follows the lengths of its replay.
+//
+// A CTA has two softmax warpgroups ("slots"), each with a 128 x 128 f32 score buffer and a
+// 128 x D accumulator in TMEM (512 columns at D = 128).  With more than 128 rows the slots
+// are the tile's two halves and share each key tile ("dual"); otherwise both hold the same
+// rows and take alternate key tiles.  One warp streams K and V tiles with TMA (128-byte
+// swizzle; the pages of a tile are copied by different lanes), one issues the MMAs, two
+// gather Q.  Step t of the issuer is O += P V of step t - 2, then S of step t into the
+// buffer it frees, so one slot's MMAs run under the other's softmax.  P replaces S in TMEM
+// as 16-bit pairs and is the A operand of P V.
+//
+// Rows of V past a length are zeroed in shared memory (a cache slot there may hold NaN, and
+// 0 * NaN would reach O); scores past a length are replaced by -inf.
+#include <math.h>
+
+#include <cudaTypedefs.h>
+
+#include "history.cuh"
+
+namespace nabla {
+
+PFN_cuTensorMapEncodeTiled_v12000 get_encode_fn();   // attn_fwd.cu
+
+namespace {
+
+constexpr int kThreads = 384;
+constexpr int kSoftmaxWarp0 = 4;          // warps 4..7 = slot 0, 8..11 = slot 1
+constexpr int kMaxCtas = 148;
+constexpr int kKeys = 128;                // keys per tile
+constexpr int kRows = 256;                // query rows per item
+constexpr int kLaunchRegs = 168;
+constexpr int kRegProducer = 56;
+constexpr int kRegSoftmax = 224;
+static_assert(128 * kRegProducer + 256 * kRegSoftmax <= kThreads * kLaunchRegs,
+              "register split exceeds the block's launch budget");
+
+// n / d and n % d for 0 <= n < 2^31 by a multiplication: m = floor(2^32 / d) + 1 overshoots
+// 2^32 / d by at most 1, so the product's high word is the quotient or one more.
+struct FastDiv {
+  uint32_t d, m;
+  __host__ void init(uint32_t v) {
+    d = v;
+    m = v > 1 ? static_cast<uint32_t>((1ull << 32) / v) + 1u : 0u;
+  }
+  __device__ __forceinline__ int div(int n, int* rem) const {
+    if (d == 1) {
+      *rem = 0;
+      return n;
+    }
+    int q = static_cast<int>(__umulhi(static_cast<uint32_t>(n), m));
+    int r = n - q * static_cast<int>(d);
+    if (r < 0) {
+      --q;
+      r += static_cast<int>(d);
+    }
+    *rem = r;
+    return q;
+  }
+};
+
+struct AttnParams {
+  // queries and outputs
+  const void* q;
+  long long q_b, q_h, q_s;
+  void* o;
+  long long o_b, o_h, o_s;
+  int o_f32;
+  float* lse;
+  const void* part_o;
+  long long po_b, po_h, po_s;
+  int part_f32;
+  const float* part_lse;
+  int B, Hq, Hkv, G, Sq, R;         // R = Sq * G rows per sequence and key head
+  FastDiv div_r, div_g;
+  // keys
+  const int32_t* prefix_pages;
+  const int32_t* tail_pages;
+  const int32_t* tail_len;
+  const int32_t* q_len;
+  int P, tail_width, page, page_shift, n_pages;
+  int causal;
+  float scale_log2;
+  // schedule
+  int shared;                       // shared mode
+  int n_rt;                         // row tiles: of a sequence (own), of the batch (shared)
+  int n_prefix;                     // prefix items (shared mode)
+  int n_items, whole;               // whole: rounds of whole items
+  int tail_half;                    // rows between the halves of a tail part
+  // workspace
+  uint32_t* cta_status;
+  int32_t* cta_done;                // own mode: the split item that CTA c completes, or -1
+  int32_t* first;                   // first / last CTA of an item (relative to whole * grid)
+  int32_t* last;
+  float* part_l;                    // log2 sums of parts
+  float* part_acc;                  // normalised f32 accumulators of parts
+  long long tail_base;              // row at which the tail parts start
+};
+
+struct Item {
+  int b, kvh, row0, rows;           // b = -1: rows of all sequences
+  int np, nt;                       // key tiles of the prefix and of the tail
+  bool dual;
+};
+
+__device__ __forceinline__ int clamp_len(int v, int top) { return v < 0 ? 0 : (v > top ? top : v); }
+
+__device__ __forceinline__ int queries_of(const AttnParams& p, int b) {
+  return p.q_len == nullptr ? p.Sq : clamp_len(__ldg(p.q_len + b), p.Sq);
+}
+__device__ __forceinline__ int tail_of(const AttnParams& p, int b) {
+  return p.tail_pages == nullptr ? 0 : clamp_len(__ldg(p.tail_len + b), p.tail_width * p.page);
+}
+__device__ __forceinline__ int tiles(int keys) { return (keys + kKeys - 1) / kKeys; }
+
+// Keys visible to query s of a sequence with n queries and a tail of L keys (s < n).
+__device__ __forceinline__ int visible(const AttnParams& p, int L, int n, int s) {
+  if (!p.causal) return p.P + L;
+  return max(p.P + L - n + s + 1, 0);
+}
+
+__device__ __forceinline__ Item item_of(const AttnParams& p, int i) {
+  Item t;
+  if (p.shared && i < p.n_prefix) {
+    t.b = -1;
+    t.kvh = i / p.n_rt;
+    t.row0 = (i - t.kvh * p.n_rt) * kRows;
+    t.rows = min(kRows, p.B * p.R - t.row0);
+    t.np = tiles(p.P);
+    t.nt = 0;
+    t.dual = t.rows > 128;
+    return t;
+  }
+  int j = i, rt = 0;
+  if (p.shared) {
+    j = i - p.n_prefix;
+  } else {
+    j = i / p.n_rt;
+    rt = i - j * p.n_rt;
+    if (p.causal) rt = p.n_rt - 1 - rt;       // the longest first
+  }
+  t.b = j / p.Hkv;
+  t.kvh = j - t.b * p.Hkv;
+  t.row0 = rt * kRows;
+  t.rows = min(kRows, p.R - t.row0);
+  t.dual = !p.shared || t.rows > 128;
+  const int n = queries_of(p, t.b), L = tail_of(p, t.b);
+  const int s0 = t.row0 / p.G, s1 = min((t.row0 + t.rows - 1) / p.G, n - 1);
+  t.np = t.nt = 0;
+  if (s0 < n) {
+    const int v = visible(p, L, n, s1);
+    if (!p.shared) t.np = tiles(min(p.P, v));
+    t.nt = tiles(max(v - p.P, 0));
+  }
+  return t;
+}
+__device__ __forceinline__ int units_of(const Item& t) { return max(t.np + t.nt, 1); }
+
+// A CTA's share of the work, part by part: key tiles [x0, x1) of an item.
+struct Walk {
+  int round, item, x0;
+  long long left;
+  struct Part {
+    int i;
+    Item t;
+    int x0, x1, total;
+    int n;        // key tiles of the part (0: an item without keys)
+  };
+  __device__ __forceinline__ bool next(const AttnParams& p, Part* o) {
+    if (round < p.whole) {
+      o->i = round * static_cast<int>(gridDim.x) + static_cast<int>(blockIdx.x);
+      ++round;
+      o->t = item_of(p, o->i);
+      o->x0 = 0;
+      o->x1 = o->total = units_of(o->t);
+    } else {
+      if (left <= 0) return false;
+      o->i = item;
+      o->t = item_of(p, item);
+      o->total = units_of(o->t);
+      o->x0 = x0;
+      o->x1 = static_cast<int>(min(static_cast<long long>(o->total), x0 + left));
+      left -= o->x1 - o->x0;
+      ++item;
+      x0 = 0;
+    }
+    o->n = o->t.np + o->t.nt == 0 ? 0 : o->x1 - o->x0;
+    return true;
+  }
+};
+
+struct Bars {
+  uint64_t full[8], empty[8];       // K/V stages: landed / read
+  uint64_t v_part;                  // a partial V tile landed (its tail rows are then zeroed)
+  uint64_t q_full, q_empty;
+  uint64_t s_full[2], p_full[2];    // S landed / P written
+  uint64_t o_done[2], o_free[2];    // the part's last P V landed / the accumulator was read
+  uint64_t drain;
+  uint32_t tmem;
+  int32_t start_item, start_x;
+  long long start_left;
+  int32_t warp_sum[kThreads / 32 + 1];
+};
+
+template <int D>
+struct Cfg {
+  static constexpr int kPanels = D / 64;
+  static constexpr int kTileBytes = 128 * D * 2;
+  static constexpr int kStages = D == 128 ? 5 : 8;
+  static constexpr int kOffKv = 2 * kTileBytes;
+  static constexpr int kOffBar = kOffKv + kStages * kTileBytes;
+  static constexpr int kSmemBytes = kOffBar + 1024 + static_cast<int>(sizeof(Bars));
+  static_assert(kSmemBytes <= 232448, "shared memory");
+  static __device__ __forceinline__ uint32_t col_s(int s) { return s * 128u; }
+  static __device__ __forceinline__ uint32_t col_o(int s) { return 256u + s * 128u; }
+};
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+
+// Rows of a part in the workspace (row-major: rows of D floats, and one log-sum each).
+__device__ __forceinline__ long long part_row(const AttnParams& p, int i, int cta, bool cont, int half, int row) {
+  if (!p.shared) return (static_cast<long long>(2 * cta + (cont ? 0 : 1)) * 2 + half) * 128 + row;
+  if (i < p.n_prefix) return (static_cast<long long>(i + cta) * 2 + half) * 128 + row;
+  return p.tail_base + (static_cast<long long>(i - p.n_prefix + cta) * 2 + half) * p.tail_half + row;
+}
+
+// log2(2^a + 2^b)
+__device__ __forceinline__ float join(float a, float b) {
+  const float m = fmaxf(a, b);
+  if (m == -INFINITY) return a + b;          // -inf, or NaN if one of them is
+  return m + log2f(exp2f(a - m) + exp2f(b - m));
+}
+
+template <bool F16>
+__device__ __forceinline__ float2 unpack2(uint32_t v) {
+  if constexpr (F16) return __half22float2(*reinterpret_cast<const __half2*>(&v));
+  return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xFFFF0000u));
+}
+template <bool F16>
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+  return F16 ? pack_f16x2(a, b) : pack_bf16x2(a, b);
+}
+
+template <int D, bool F16>
+__global__ void __launch_bounds__(kThreads, 1)
+    prefix_attn_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
+                       const __grid_constant__ AttnParams p) {
+  using C = Cfg<D>;
+  extern __shared__ unsigned char smem_raw[];
+  unsigned char* smem = reinterpret_cast<unsigned char*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  unsigned char* sKV = smem + C::kOffKv;
+  Bars& B = *reinterpret_cast<Bars*>(smem + C::kOffBar);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  uint32_t* status = p.cta_status + blockIdx.x;
+
+  if (threadIdx.x == 0) {
+    *status = 0;
+    p.cta_done[blockIdx.x] = -1;
+    for (int i = 0; i < C::kStages; ++i) {
+      mbar_init(&B.full[i], 1);
+      mbar_init(&B.empty[i], 1);
+    }
+    mbar_init(&B.v_part, 1);
+    mbar_init(&B.q_full, 64);
+    mbar_init(&B.q_empty, 1);
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&B.s_full[s], 1);
+      mbar_init(&B.p_full[s], 128);
+      mbar_init(&B.o_done[s], 1);
+      mbar_init(&B.o_free[s], 128);
+    }
+    mbar_init(&B.drain, 1);
+    fence_mbarrier_init();
+    B.start_left = 0;
+    B.start_item = B.start_x = 0;
+  }
+  if (warp == 1) {
+    tmem_alloc(&B.tmem, 512);
+    tmem_relinquish();
+  }
+  // The run of units of this CTA among the items that no round hands out whole: a block-wide
+  // scan of their lengths, then the thread whose items hold the run's start finds it.
+  {
+    const int i0 = p.whole * static_cast<int>(gridDim.x);
+    const int n = p.n_items - i0;
+    const int per = (n + kThreads - 1) / kThreads;
+    const int a = min(static_cast<int>(threadIdx.x) * per, n), b = min(a + per, n);
+    int sum = 0;
+    for (int i = a; i < b; ++i) sum += units_of(item_of(p, i0 + i));
+    int inc = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += v;
+    }
+    if (lane == 31) B.warp_sum[warp] = inc;
+    __syncthreads();
+    int before = 0, total = 0;
+    for (int w = 0; w < kThreads / 32; ++w) {
+      if (w < warp) before += B.warp_sum[w];
+      total += B.warp_sum[w];
+    }
+    // every run has at least one unit, so the parts of an item are those of neighbouring CTAs
+    const int runs = min(total, static_cast<int>(gridDim.x)), run = min(static_cast<int>(blockIdx.x), runs);
+    const long long u0 = runs > 0 ? static_cast<long long>(total) * run / runs : 0;
+    const long long u1 = run < runs ? static_cast<long long>(total) * (run + 1) / runs : u0;
+    int at = before + inc - sum;                 // units before this thread's items
+    if (u1 > u0 && u0 >= at && u0 < at + sum) {
+      int i = a, len = 0;
+      for (; i < b; ++i) {
+        len = units_of(item_of(p, i0 + i));
+        if (u0 < at + len) break;
+        at += len;
+      }
+      B.start_item = i0 + i;
+      B.start_x = static_cast<int>(u0 - at);
+      B.start_left = u1 - u0;
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = B.tmem;
+  Walk walk;
+  walk.round = 0;
+  walk.item = B.start_item;
+  walk.x0 = B.start_x;
+  walk.left = B.start_left;
+  Walk::Part part;
+
+  if (warp < kSoftmaxWarp0) {
+    reg_dealloc<kRegProducer>();
+    if (warp == 0) {
+      // ------------------------------------------------------------------ K and V tiles
+      // A tile is K then V, in successive stages of one ring.  Its pages (or, for large
+      // pages, its one page) are copied by different lanes, panel by panel.
+      if (lane == 0) {
+        tma_prefetch_desc(&map_k);
+        tma_prefetch_desc(&map_v);
+      }
+      const int rows_pp = min(p.page, kKeys);            // rows per piece
+      const int piece = lane / C::kPanels, panel = lane % C::kPanels;
+      long long g = 0;          // stages filled
+      long long n_part = 0;     // partial V tiles
+      bool ok = true;
+      auto wait_all = [&](uint64_t* bar, uint32_t parity, uint32_t code) -> bool {
+        return __all_sync(0xffffffffu, mbar_wait(bar, parity, status, code));
+      };
+      while (ok && walk.next(p, &part)) {
+        const int L = part.t.b >= 0 ? tail_of(p, part.t.b) : 0;
+        // Page of this lane's piece of tile x (-1: past the length, nothing to copy).
+        auto lookup = [&](int x) -> int {
+          const bool pre = x < part.t.np;
+          const int base = (pre ? x : x - part.t.np) * kKeys + piece * rows_pp;
+          if (piece * rows_pp >= kKeys || base >= (pre ? p.P : L)) return -1;
+          const int32_t* list = pre ? p.prefix_pages : p.tail_pages + static_cast<long long>(part.t.b) * p.tail_width;
+          const int id = __ldg(list + (base >> p.page_shift));
+          if (id < 0 || id >= p.n_pages) {
+            record_status(status, kDevBadPage);
+            return p.n_pages;                            // out of bounds: the copy fills zeros
+          }
+          return id;
+        };
+        const int xe = part.x0 + part.n;
+        int id = part.n > 0 ? lookup(part.x0) : -1;
+        for (int x = part.x0; ok && x < xe; ++x) {
+          const bool pre = x < part.t.np;
+          const int base = (pre ? x : x - part.t.np) * kKeys;
+          const int valid = min((pre ? p.P : L) - base, kKeys);
+          const uint32_t bytes = static_cast<uint32_t>((valid + rows_pp - 1) / rows_pp * rows_pp) * D * 2;
+          const int slot = (base + piece * rows_pp) & (p.page - 1);
+          const int cur = id;
+          if (x + 1 < xe) id = lookup(x + 1);
+#pragma unroll
+          for (int kv = 0; kv < 2; ++kv) {
+            const int st = static_cast<int>(g % C::kStages);
+            if (g >= C::kStages &&
+                !wait_all(&B.empty[st], (g / C::kStages - 1) & 1, kDevTimeoutKvEmpty)) {
+              ok = false;
+              break;
+            }
+            unsigned char* dst = sKV + st * C::kTileBytes;
+            const bool cut = kv == 1 && valid < kKeys;
+            uint64_t* bar = cut ? &B.v_part : &B.full[st];
+            if (lane == 0) mbar_arrive_expect_tx(bar, bytes);
+            __syncwarp();
+            if (cur >= 0)
+              tma_load_4d(dst + panel * 16384 + piece * rows_pp * 128, kv ? &map_v : &map_k, bar, panel * 64, slot,
+                          part.t.kvh, cur);
+            __syncwarp();
+            if (cut) {
+              if (!wait_all(&B.v_part, n_part & 1, kDevTimeoutTmaFull)) {
+                ok = false;
+                break;
+              }
+              ++n_part;
+              for (int e = valid * 8 + lane; e < kKeys * 8; e += 32)
+#pragma unroll
+                for (int pn = 0; pn < C::kPanels; ++pn)
+                  *reinterpret_cast<uint4*>(dst + pn * 16384 + e * 16) = make_uint4(0u, 0u, 0u, 0u);
+              fence_proxy_async_smem();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&B.full[st]);
+              __syncwarp();
+            }
+            ++g;
+          }
+        }
+      }
+      // Copies still in flight must land before the CTA exits.
+      for (long long x = g > C::kStages ? g - C::kStages : 0; x < g; ++x)
+        mbar_wait(&B.full[x % C::kStages], (x / C::kStages) & 1, status, kDevTimeoutDrain);
+      __syncwarp();
+    } else if (warp == 1) {
+      // ------------------------------------------------------------------ MMA issuer
+      if (lane == 0) {
+        constexpr uint32_t idesc_s = F16 ? idesc_f16_f32(128, 128, false, false) : idesc_bf16_f32(128, 128, false, false);
+        constexpr uint32_t idesc_o = F16 ? idesc_f16_f32(128, D, false, true) : idesc_bf16_f32(128, D, false, true);
+        const uint32_t q_addr = smem_u32(smem), kv_addr = smem_u32(sKV);
+        long long g0 = 0;               // stages of earlier parts
+        long long n_q = 0;              // parts with keys
+        long long n_p[2] = {0, 0};      // P V issued per slot
+        long long n_o[2] = {0, 0};      // parts finished per slot
+        bool ok = true;
+        auto full = [&](long long g) -> bool {
+          return mbar_wait(&B.full[g % C::kStages], (g / C::kStages) & 1, status, kDevTimeoutTmaFull);
+        };
+        while (ok && walk.next(p, &part)) {
+          if (part.n == 0) continue;
+          const int dual = part.t.dual ? 1 : 0;
+          const int steps = part.n << dual;
+          if (!mbar_wait(&B.q_full, n_q & 1, status, kDevTimeoutQFull)) break;
+          ++n_q;
+          for (int t = 0; t < steps + 2; ++t) {
+            const int s = t & 1;
+            if (t >= 2) {
+              // O += P V of step t - 2 (same slot)
+              const int x = (t - 2) >> dual;
+              const long long gv = g0 + 2 * x + 1;
+              const bool first = dual ? x == 0 : x < 2;
+              if (!mbar_wait(&B.p_full[s], n_p[s] & 1, status, kDevTimeoutPFull) || !full(gv) ||
+                  (first && n_o[s] > 0 && !mbar_wait(&B.o_free[s], (n_o[s] - 1) & 1, status, kDevTimeoutOBar))) {
+                ok = false;
+                break;
+              }
+              ++n_p[s];
+              tc_fence_after();
+              const uint32_t v = kv_addr + static_cast<uint32_t>(gv % C::kStages) * C::kTileBytes;
+#pragma unroll
+              for (int kk = 0; kk < kKeys / 16; ++kk) {
+                const uint64_t bd = sdesc_sw128(v + kk * 2048, 16384, 1024);
+                mma_bf16_ts(tmem + C::col_o(s), tmem + C::col_s(s) + kk * 8, bd, idesc_o, (!first || kk > 0) ? 1u : 0u);
+              }
+              if (!dual || s == 1) mma_commit(&B.empty[gv % C::kStages]);
+              if (t >= steps) {          // the slot's last step
+                mma_commit(&B.o_done[s]);
+                ++n_o[s];
+              }
+            }
+            if (t < steps) {
+              const int x = t >> dual;
+              const long long gk = g0 + 2 * x;
+              if (!full(gk)) {
+                ok = false;
+                break;
+              }
+              tc_fence_after();
+              const uint32_t qs = q_addr + (dual ? s : 0) * C::kTileBytes;
+              const uint32_t k = kv_addr + static_cast<uint32_t>(gk % C::kStages) * C::kTileBytes;
+#pragma unroll
+              for (int kk = 0; kk < D / 16; ++kk) {
+                const uint32_t off = (kk >> 2) * 16384 + (kk & 3) * 32;
+                mma_bf16_ss(tmem + C::col_s(s), sdesc_sw128(qs + off, 16, 1024), sdesc_sw128(k + off, 16, 1024), idesc_s,
+                            kk > 0 ? 1u : 0u);
+              }
+              mma_commit(&B.s_full[s]);
+              if (!dual || s == 1) mma_commit(&B.empty[gk % C::kStages]);
+              if (t == steps - 1) mma_commit(&B.q_empty);
+            }
+          }
+          g0 += 2 * part.n;
+        }
+        mma_commit(&B.drain);
+        mbar_wait(&B.drain, 0, status, kDevTimeoutDrain);
+      }
+      __syncwarp();
+    } else {
+      // ------------------------------------------------------------------ Q rows
+      // 64 threads gather the tile's rows into the K-major 128-byte-swizzled layout, a row by
+      // D / 8 neighbouring threads; rows that do not exist are zeros.
+      constexpr int kChunks = D / 8;
+      const int tid = threadIdx.x - 64;
+      const int c = tid % kChunks, r_first = tid / kChunks;
+      constexpr int kStep = 64 / kChunks;
+      const uint16_t* q = static_cast<const uint16_t*>(p.q);
+      long long n_q = 0;
+      bool ok = true;
+      while (ok && walk.next(p, &part)) {
+        if (part.n == 0) continue;
+        const int n_rows = part.t.dual ? 256 : 128;
+        if (n_q > 0) ok = __all_sync(0xffffffffu, mbar_wait(&B.q_empty, (n_q - 1) & 1, status, kDevTimeoutQFull));
+        if (!ok) break;
+        ++n_q;
+        for (int r = r_first; r < n_rows; r += kStep) {
+          unsigned char* dst = smem + (r >> 7) * C::kTileBytes + (c >> 3) * 16384 + (r & 127) * 128 +
+                               (((c & 7) ^ (r & 7)) << 4);
+          if (r < part.t.rows) {
+            int b = part.t.b, rr = part.t.row0 + r, g;
+            if (b < 0) b = p.div_r.div(rr, &rr);
+            const int s = p.div_g.div(rr, &g);
+            cp_async16(smem_u32(dst), q + b * p.q_b + (part.t.kvh * p.G + g) * p.q_h + s * p.q_s + c * 8);
+          } else {
+            *reinterpret_cast<uint4*>(dst) = make_uint4(0u, 0u, 0u, 0u);
+          }
+        }
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        fence_proxy_async_smem();
+        mbar_arrive(&B.q_full);
+      }
+      __syncwarp();
+    }
+  } else {
+    reg_alloc<kRegSoftmax>();
+    // -------------------------------------------------------------------- softmax of a slot
+    const int slot = (warp - kSoftmaxWarp0) >> 2;
+    const int row = ((warp - kSoftmaxWarp0) & 3) * 32 + lane;       // TMEM lane
+    const uint32_t lane_base = static_cast<uint32_t>(((warp - kSoftmaxWarp0) & 3) * 32) << 16;
+    const uint32_t s_col = tmem + lane_base + C::col_s(slot);
+    const uint32_t o_col = tmem + lane_base + C::col_o(slot);
+    const float sl2 = p.scale_log2;
+    const float2 sl2v = make_float2(sl2, sl2);
+    // The largest weight of a row lies in [2^kBias, 2^(kBias + 8)]: for fp16 as high as its
+    // range allows, so that weights down to 2^-31 of it are kept (2^-24 without the bias; a
+    // long prefix has enough small ones to matter).
+    constexpr float kBias = F16 ? 7.0f : 0.0f;
+    long long n_s = 0, n_o = 0;
+    bool ok = true;
+    while (ok && walk.next(p, &part)) {
+      // the row: its sequence, query and head, and the keys it sees
+      const int r = part.t.dual ? slot * 128 + row : row;
+      int b = part.t.b, s = 0, gh = 0;
+      bool valid = r < part.t.rows;
+      int lim_p = 0x7FFFFFFF, lim_t = 0x7FFFFFFF;     // rows that are never written need no mask
+      if (valid) {
+        int rr = part.t.row0 + r;
+        if (b < 0) b = p.div_r.div(rr, &rr);
+        s = p.div_g.div(rr, &gh);
+        const int n = queries_of(p, b), L = tail_of(p, b);
+        valid = s < n;
+        if (valid) {
+          const int v = visible(p, L, n, s);
+          lim_p = min(v, p.P);
+          lim_t = v - p.P;
+        }
+      }
+      const int stride = part.t.dual ? 1 : 2;
+      const int x_first = part.x0 + (part.t.dual ? 0 : slot);
+      const int xe = part.x0 + part.n;
+      float m_ref = -INFINITY, l = 0.f;
+      bool any = false;
+      for (int x = x_first; x < xe; x += stride) {
+        any = true;
+        ok = __all_sync(0xffffffffu, mbar_wait(&B.s_full[slot], n_s & 1, status, kDevTimeoutSFull));
+        if (!ok) break;
+        tc_fence_after();
+        uint32_t sv[128];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) tmem_ld32(s_col + 32 * i, *reinterpret_cast<uint32_t(*)[32]>(&sv[32 * i]));
+        tmem_wait_ld();
+#pragma unroll
+        for (int i = 0; i < 4; ++i) reg_fence32(*reinterpret_cast<uint32_t(*)[32]>(&sv[32 * i]));
+        const int seen = x < part.t.np ? lim_p - x * kKeys : lim_t - (x - part.t.np) * kKeys;
+        if (__any_sync(0xffffffffu, seen < kKeys)) {
+#pragma unroll
+          for (int i = 0; i < 128; ++i) sv[i] = i < seen ? sv[i] : 0xFF800000u;
+        }
+        float m8[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) m8[i] = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < 128; i += 2)
+          m8[(i >> 1) & 7] = fmax3(m8[(i >> 1) & 7], __uint_as_float(sv[i]), __uint_as_float(sv[i + 1]));
+        const float mx = fmaxf(fmaxf(fmaxf(m8[0], m8[1]), fmaxf(m8[2], m8[3])),
+                               fmaxf(fmaxf(m8[4], m8[5]), fmaxf(m8[6], m8[7])));
+        float factor = 1.f;
+        bool rescale = false;
+        const float rm = mx * sl2 - kBias;
+        if (mx != -INFINITY && rm > m_ref + 8.0f) {
+          if (m_ref != -INFINITY) {
+            factor = fast_exp2(m_ref - rm);
+            rescale = true;
+          }
+          m_ref = rm;
+        }
+        const float neg = m_ref == -INFINITY ? 0.f : -m_ref;
+        const float2 negv = make_float2(neg, neg);
+        float2 acc = make_float2(0.f, 0.f);
+#pragma unroll
+        for (int e = 0; e < 64; ++e) {
+          const float2 y = __ffma2_rn(make_float2(__uint_as_float(sv[2 * e]), __uint_as_float(sv[2 * e + 1])), sl2v, negv);
+          const float2 pr = make_float2(fast_exp2(y.x), fast_exp2(y.y));
+          acc = __fadd2_rn(acc, pr);
+          sv[e] = pack2<F16>(pr.x, pr.y);
+        }
+        tmem_st32(s_col, *reinterpret_cast<uint32_t(*)[32]>(&sv[0]));
+        tmem_st32(s_col + 32, *reinterpret_cast<uint32_t(*)[32]>(&sv[32]));
+        // Every earlier P V of the slot was issued before this S, so its completion covers
+        // them: the accumulator may be rescaled at once.
+        if (__any_sync(0xffffffffu, rescale)) {
+#pragma unroll 1
+          for (int o0 = 0; o0 < D; o0 += 16) {
+            uint32_t ov[16];
+            tmem_ld16(o_col + o0, ov);
+            tmem_wait_ld();
+            reg_fence16(ov);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) ov[i] = __float_as_uint(__uint_as_float(ov[i]) * factor);
+            tmem_st16(o_col + o0, ov);
+          }
+        }
+        l = l * factor + (acc.x + acc.y);
+        tmem_wait_st();
+        tc_fence_before();
+        mbar_arrive(&B.p_full[slot]);
+        ++n_s;
+      }
+      if (!ok) break;
+      // ------------------------------------------------------------------ the part's result
+      if (any) {
+        ok = __all_sync(0xffffffffu, mbar_wait(&B.o_done[slot], n_o & 1, status, kDevTimeoutOBar));
+        if (!ok) break;
+        ++n_o;
+        tc_fence_after();
+      }
+      // l is NaN where a visible score is: such a row is NaN, not empty
+      float inv = l == 0.f ? 0.f : 1.f / l;
+      float sum2 = l == 0.f ? -INFINITY : m_ref + log2f(l);
+      const bool whole = !p.shared && part.x0 == 0 && part.x1 == part.total;
+      const float* prow = nullptr;
+      const uint16_t* prow16 = nullptr;
+      float pw = 0.f;
+      float* wrow = nullptr;
+      unsigned char* orow = nullptr;
+      if (whole) {
+        if (valid) {
+          const int h = part.t.kvh * p.G + gh;
+          const long long flat = (static_cast<long long>(b) * p.Hq + h) * p.Sq + s;
+          if (p.part_lse != nullptr) {
+            const float a = p.part_lse[flat] * 1.4426950408889634f;
+            if (a != -INFINITY) {
+              const float both = join(sum2, a);
+              inv *= sum2 == -INFINITY ? 0.f : exp2f(sum2 - both);
+              pw = exp2f(a - both);
+              sum2 = both;
+              const long long off = b * p.po_b + h * p.po_h + s * p.po_s;
+              if (p.part_f32) prow = static_cast<const float*>(p.part_o) + off;
+              else prow16 = static_cast<const uint16_t*>(p.part_o) + off;
+            }
+          }
+          if (p.lse != nullptr) p.lse[flat] = sum2 * 0.69314718055994531f;
+          orow = static_cast<unsigned char*>(p.o) + (b * p.o_b + h * p.o_h + s * p.o_s) * (p.o_f32 ? 4 : 2);
+        }
+      } else {
+        if (part.x0 == 0 && threadIdx.x == kSoftmaxWarp0 * 32) p.first[part.i - p.whole * gridDim.x] = blockIdx.x;
+        if (part.x1 == part.total && threadIdx.x == kSoftmaxWarp0 * 32) {
+          p.last[part.i - p.whole * gridDim.x] = blockIdx.x;
+          if (!p.shared && part.x0 > 0) p.cta_done[blockIdx.x] = part.i;
+        }
+        if (valid) {
+          const long long w = part_row(p, part.i, blockIdx.x, part.x0 > 0, slot, row);
+          p.part_l[w] = sum2;
+          if (sum2 != -INFINITY) wrow = p.part_acc + w * D;
+        }
+      }
+#pragma unroll 1
+      for (int d0 = 0; d0 < D; d0 += 32) {
+        uint32_t a[32];
+        if (any) {
+          tmem_ld32(o_col + d0, a);
+          tmem_wait_ld();
+          reg_fence32(a);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) a[i] = 0u;
+        }
+        if (any && d0 + 32 == D) {
+          tc_fence_before();
+          mbar_arrive(&B.o_free[slot]);
+        }
+        float f[32];
+#pragma unroll
+        for (int i = 0; i < 32; ++i) f[i] = inv == 0.f ? 0.f : __uint_as_float(a[i]) * inv;
+        if (prow != nullptr) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const float4 y = *reinterpret_cast<const float4*>(prow + d0 + 4 * i);
+            f[4 * i] += pw * y.x; f[4 * i + 1] += pw * y.y; f[4 * i + 2] += pw * y.z; f[4 * i + 3] += pw * y.w;
+          }
+        } else if (prow16 != nullptr) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const uint4 y = *reinterpret_cast<const uint4*>(prow16 + d0 + 8 * i);
+            const uint32_t w[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const float2 z = unpack2<F16>(w[j]);
+              f[8 * i + 2 * j] += pw * z.x;
+              f[8 * i + 2 * j + 1] += pw * z.y;
+            }
+          }
+        }
+        float4* w4 = wrow != nullptr ? reinterpret_cast<float4*>(wrow + d0)
+                     : (orow != nullptr && p.o_f32) ? reinterpret_cast<float4*>(orow + d0 * 4) : nullptr;
+        if (w4 != nullptr) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) w4[i] = make_float4(f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3]);
+        } else if (orow != nullptr) {
+          uint4* o4 = reinterpret_cast<uint4*>(orow + d0 * 2);
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            o4[i] = make_uint4(pack2<F16>(f[8 * i], f[8 * i + 1]), pack2<F16>(f[8 * i + 2], f[8 * i + 3]),
+                               pack2<F16>(f[8 * i + 4], f[8 * i + 5]), pack2<F16>(f[8 * i + 6], f[8 * i + 7]));
+        }
+      }
+    }
+  }
+  // ---------------------------------------------------------------------- teardown
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// Joins the parts of split items, one warp per row, in the order of their keys' CTAs
+// (deterministic), merges the caller's part and writes the row.  Block 0 also gathers the
+// CTAs' status words and looks the lengths over.
+constexpr int kJoinWarps = 8;
+
+template <int D, bool F16>
+__global__ void __launch_bounds__(kJoinWarps * 32) prefix_join_kernel(const __grid_constant__ AttnParams p,
+                                                                      uint32_t* status, int ctas) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (blockIdx.x == 0 && blockIdx.y == 0 && warp == 0) {
+    uint32_t w = 0;
+    for (int c = lane; c < ctas; c += 32)
+      if (w == 0) w = p.cta_status[c];
+    for (int i = lane; i < p.B; i += 32) {
+      if (p.q_len != nullptr && queries_of(p, i) != p.q_len[i] && w == 0) w = kDevBadLength;
+      if (p.tail_pages != nullptr && tail_of(p, i) != p.tail_len[i] && w == 0) w = kDevBadLength;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      const uint32_t v = __shfl_xor_sync(0xffffffffu, w, o);
+      if (w == 0) w = v;
+    }
+    if (lane == 0) *status = w;
+  }
+  // the row, and up to two items that hold parts of it
+  int it[2] = {-1, -1}, lrow[2] = {0, 0};
+  bool alt[2] = {false, false};
+  int b, kvh, rr;
+  if (p.shared) {
+    const long long id = static_cast<long long>(blockIdx.x) * kJoinWarps + warp;
+    if (id >= static_cast<long long>(p.Hkv) * p.B * p.R) return;
+    const int per = p.B * p.R;
+    kvh = static_cast<int>(id / per);
+    const int rg = static_cast<int>(id - static_cast<long long>(kvh) * per);
+    b = p.div_r.div(rg, &rr);
+    if (p.n_prefix > 0) {
+      const int rt = rg / kRows;
+      it[0] = kvh * p.n_rt + rt;
+      lrow[0] = rg - rt * kRows;
+      alt[0] = min(kRows, per - rt * kRows) <= 128;
+    }
+    if (p.tail_pages != nullptr) {
+      it[1] = p.n_prefix + b * p.Hkv + kvh;
+      lrow[1] = rr;
+      alt[1] = p.R <= 128;
+    }
+  } else {
+    const int i = p.cta_done[blockIdx.x];
+    if (i < 0) return;
+    const Item t = item_of(p, i);
+    const int r = blockIdx.y * kJoinWarps + warp;
+    if (r >= t.rows) return;
+    b = t.b;
+    kvh = t.kvh;
+    rr = t.row0 + r;
+    it[0] = i;
+    lrow[0] = r;
+  }
+  int gh;
+  const int s = p.div_g.div(rr, &gh);
+  if (s >= queries_of(p, b)) return;
+  int first[2] = {0, 0}, n[2] = {0, 0};
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    if (it[k] < 0) continue;
+    const int e = it[k] - p.whole * ctas;
+    first[k] = p.first[e];
+    const int last = p.last[e];
+    if (first[k] < 0 || last < first[k] || last >= ctas) return;     // only after a wait gave up
+    n[k] = (last - first[k] + 1) * (alt[k] ? 2 : 1);
+  }
+  auto where = [&](int j) -> long long {
+    const int k = j < n[0] ? 0 : 1;
+    const int q = j - (k ? n[0] : 0);
+    const int c = first[k] + (alt[k] ? q >> 1 : q);
+    const int half = alt[k] ? (q & 1) : lrow[k] >> 7;
+    return part_row(p, it[k], c, c > first[k], half, alt[k] ? lrow[k] : lrow[k] & 127);
+  };
+  const int total = n[0] + n[1];
+  float m = -INFINITY;
+  bool nan = false;
+  for (int j = lane; j < total; j += 32) {
+    const float v = p.part_l[where(j)];
+    nan |= v != v;
+    m = fmaxf(m, v);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  nan = __any_sync(0xffffffffu, nan);
+  float sum = 0.f;
+  constexpr int kPer = D / 32;
+  float acc[kPer];
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) acc[i] = 0.f;
+  if (m != -INFINITY) {
+#pragma unroll 4
+    for (int j = 0; j < total; ++j) {
+      const long long w = where(j);
+      const float v = p.part_l[w];
+      if (v == -INFINITY) continue;
+      const float e = exp2f(v - m);
+      sum += e;
+      const float* src = p.part_acc + w * D + lane * kPer;
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) acc[i] += e * src[i];
+    }
+  }
+  float lse2 = m == -INFINITY ? -INFINITY : m + log2f(sum);
+  if (nan) lse2 = __int_as_float(0x7FC00000);
+  const float inv = nan ? lse2 : (sum > 0.f ? 1.f / sum : 0.f);
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) acc[i] *= inv;
+  const int h = kvh * p.G + gh;
+  const long long flat = (static_cast<long long>(b) * p.Hq + h) * p.Sq + s;
+  if (p.part_lse != nullptr) {
+    const float a = p.part_lse[flat] * 1.4426950408889634f;
+    if (a != -INFINITY) {
+      const float both = join(lse2, a);
+      const float wa = lse2 == -INFINITY ? 0.f : exp2f(lse2 - both), wb = exp2f(a - both);
+      const long long off = b * p.po_b + h * p.po_h + s * p.po_s + lane * kPer;
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) {
+        float y;
+        if (p.part_f32) {
+          y = static_cast<const float*>(p.part_o)[off + i];
+        } else if (F16) {
+          y = __half2float(static_cast<const __half*>(p.part_o)[off + i]);
+        } else {
+          y = __bfloat162float(static_cast<const __nv_bfloat16*>(p.part_o)[off + i]);
+        }
+        acc[i] = acc[i] * wa + y * wb;
+      }
+      lse2 = both;
+    }
+  }
+  __syncwarp();
+  if (p.lse != nullptr && lane == 0) p.lse[flat] = lse2 * 0.69314718055994531f;
+  const long long off = b * p.o_b + h * p.o_h + s * p.o_s + lane * kPer;
+  if (p.o_f32) {
+    float* o = static_cast<float*>(p.o) + off;
+#pragma unroll
+    for (int i = 0; i < kPer; i += 2) *reinterpret_cast<float2*>(o + i) = make_float2(acc[i], acc[i + 1]);
+  } else {
+    uint32_t* o = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.o) + off);
+#pragma unroll
+    for (int i = 0; i < kPer; i += 2) o[i / 2] = pack2<F16>(acc[i], acc[i + 1]);
+  }
+}
+
+// 4-D map of a pool [n_pages, H, page, D]: box = 64 channels x min(page, 128) tokens of one
+// head of one page, 128-byte swizzle; a page number of n_pages fills zeros.
+bool make_map_pool(CUtensorMap* map, const void* base, const nabla_cache& c) {
+  PFN_cuTensorMapEncodeTiled_v12000 enc = get_encode_fn();
+  if (!enc) return false;
+  const cuuint64_t row = static_cast<cuuint64_t>(c.D) * 2;
+  cuuint64_t dims[4] = {static_cast<cuuint64_t>(c.D), static_cast<cuuint64_t>(c.page),
+                        static_cast<cuuint64_t>(c.H), static_cast<cuuint64_t>(c.n_pages)};
+  cuuint64_t strides[3] = {row, row * c.page, row * c.page * c.H};
+  cuuint32_t box[4] = {64u, static_cast<cuuint32_t>(c.page < kKeys ? c.page : kKeys), 1u, 1u};
+  cuuint32_t estr[4] = {1u, 1u, 1u, 1u};
+  return enc(map, c.dtype == NABLA_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4,
+             const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// How a call is cut into items, and its workspace.
+struct Plan {
+  bool shared;
+  long long n_rt, n_prefix, n_tail, n_items;
+  long long prefix_rows, tail_rows;      // rows of parts
+  size_t off_first, off_last, off_l, off_acc, bytes;
+};
+
+Plan make_plan(long long B, long long Hkv, long long G, long long Sq, int D) {
+  Plan a;
+  const long long R = G * Sq;
+  a.shared = R < kRows;
+  if (a.shared) {
+    a.n_rt = (B * R + kRows - 1) / kRows;
+    a.n_prefix = Hkv * a.n_rt;
+    a.n_tail = B * Hkv;
+    a.n_items = a.n_prefix + a.n_tail;
+    a.prefix_rows = (a.n_prefix + kMaxCtas) * kRows;
+    a.tail_rows = (a.n_tail + kMaxCtas) * 2 * (R < 128 ? R : 128);
+  } else {
+    a.n_rt = (R + kRows - 1) / kRows;
+    a.n_prefix = a.n_tail = 0;
+    a.n_items = B * Hkv * a.n_rt;
+    a.prefix_rows = 2LL * kMaxCtas * kRows;
+    a.tail_rows = 0;
+  }
+  const long long split = a.shared ? a.n_items : kMaxCtas;
+  a.off_first = kStatusBytes + 2 * 1024;
+  a.off_last = a.off_first + align_up(split * 4, 256);
+  a.off_l = a.off_last + align_up(split * 4, 256);
+  a.off_acc = a.off_l + align_up((a.prefix_rows + a.tail_rows) * 4, 256);
+  a.bytes = a.off_acc + static_cast<size_t>(a.prefix_rows + a.tail_rows) * D * 4;
+  return a;
+}
+
+nabla_status check_sizes(int64_t B, int64_t Hq, int64_t Hkv, int64_t Sq, int D) {
+  if (B < 1 || Hq < 1 || Hkv < 1 || Sq < 1 || Hq % Hkv) return NABLA_ERR_INVALID_ARG;
+  if (D != 64 && D != 128) return NABLA_ERR_UNSUPPORTED;
+  // rows of a key head, items and their units are counted in 32 bits
+  const double rows = static_cast<double>(B) * (Hq / Hkv) * Sq;
+  if (rows >= 1073741824.0 || static_cast<double>(B) * Hkv + rows / 256 * Hkv >= 1048576.0 * 8) return NABLA_ERR_UNSUPPORTED;
+  return NABLA_OK;
+}
+
+template <int D, bool F16>
+nabla_status launch(const AttnParams& p, const nabla_cache& cache, uint32_t* status, cudaStream_t st) {
+  using C = Cfg<D>;
+  CUtensorMap mk, mv;
+  if (!make_map_pool(&mk, cache.k, cache) || !make_map_pool(&mv, cache.v, cache)) return NABLA_ERR_CUDA;
+  cudaError_t e = cudaFuncSetAttribute(prefix_attn_kernel<D, F16>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
+  if (e != cudaSuccess) return cuda_status(e);
+  // The register split needs the block to launch with kLaunchRegs a thread.
+  cudaFuncAttributes fa;
+  e = cudaFuncGetAttributes(&fa, prefix_attn_kernel<D, F16>);
+  if (e != cudaSuccess) return cuda_status(e);
+  if (fa.numRegs != kLaunchRegs) return NABLA_ERR_UNSUPPORTED;
+  int dev = 0, sms = kMaxCtas;
+  e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess) return cuda_status(e);
+  const int ctas = sms < kMaxCtas ? sms : kMaxCtas;
+  AttnParams a = p;
+  a.whole = a.shared ? 0 : a.n_items / ctas;
+  prefix_attn_kernel<D, F16><<<ctas, kThreads, C::kSmemBytes, st>>>(mk, mv, a);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return cuda_status(e);
+  dim3 grid(ctas, kRows / kJoinWarps);
+  if (a.shared) {
+    const long long rows = static_cast<long long>(a.Hkv) * a.B * a.R;
+    grid = dim3(static_cast<unsigned>((rows + kJoinWarps - 1) / kJoinWarps));
+  }
+  prefix_join_kernel<D, F16><<<grid, kJoinWarps * 32, 0, st>>>(a, status, ctas);
+  return cuda_status(cudaGetLastError());
+}
+
+}  // namespace
+}  // namespace nabla
+
+using namespace nabla;
+
+extern "C" size_t nabla_prefix_workspace_bytes(int32_t B, int32_t Hq, int32_t Hkv, int32_t Sq, int32_t D) {
+  if (check_sizes(B, Hq, Hkv, Sq, D) != NABLA_OK) return 0;
+  return make_plan(B, Hkv, Hq / Hkv, Sq, D).bytes;
+}
+
+extern "C" nabla_status nabla_prefix_attn(nabla_heads q, int32_t B, int32_t Sq, nabla_cache cache,
+                                          const int32_t* prefix_pages, int32_t prefix_len,
+                                          const int32_t* tail_pages, int32_t tail_width, const int32_t* tail_len,
+                                          const int32_t* q_len, int32_t causal, float scale, nabla_heads part_o,
+                                          const float* part_lse, nabla_heads o, float* lse, void* workspace,
+                                          size_t workspace_bytes, nabla_stream_t stream) {
+  nabla_status rc = check_cache(cache);
+  if (rc != NABLA_OK) return rc;
+  if ((rc = check_sizes(B, q.H, cache.H, Sq, cache.D)) != NABLA_OK) return rc;
+  if ((rc = check_heads(q, B, Sq, false)) != NABLA_OK || (rc = check_heads(o, B, Sq, true)) != NABLA_OK) return rc;
+  if (q.dtype != cache.dtype || o.H != q.H) return NABLA_ERR_INVALID_ARG;
+  if (o.dtype != q.dtype && o.dtype != NABLA_F32) return NABLA_ERR_INVALID_ARG;
+  if (prefix_len < 0 || (prefix_len > 0 && !prefix_pages)) return NABLA_ERR_INVALID_ARG;
+  if (tail_pages ? (tail_width < 1 || !tail_len) : (tail_len != nullptr)) return NABLA_ERR_INVALID_ARG;
+  const int64_t tail_cap = tail_pages ? static_cast<int64_t>(tail_width) * cache.page : 0;
+  if (prefix_len + tail_cap + Sq > 2147483000LL) return NABLA_ERR_UNSUPPORTED;
+  if (causal != 0 && causal != 1) return NABLA_ERR_INVALID_ARG;
+  if (!(scale > 0.f) || !isfinite(scale)) return NABLA_ERR_INVALID_ARG;
+  for (const void* x : {static_cast<const void*>(prefix_pages), static_cast<const void*>(tail_pages),
+                        static_cast<const void*>(tail_len), static_cast<const void*>(q_len),
+                        static_cast<const void*>(part_lse), static_cast<const void*>(lse)})
+    if (reinterpret_cast<uintptr_t>(x) & 3) return NABLA_ERR_INVALID_ARG;
+  // units of work are summed in 32 bits
+  const double rows = static_cast<double>(B) * (q.H / cache.H) * Sq;
+  const double keys = static_cast<double>(prefix_len) + static_cast<double>(tail_cap);
+  if ((rows / 256 + B + 1) * cache.H * (keys / 128 + 2) >= 2147483648.0) return NABLA_ERR_UNSUPPORTED;
+  const bool part = part_o.ptr != nullptr;
+  if (part != (part_lse != nullptr)) return NABLA_ERR_INVALID_ARG;
+  if (part) {
+    if ((rc = check_heads(part_o, B, Sq, false)) != NABLA_OK) return rc;
+    if (part_o.H != q.H || (part_o.dtype != NABLA_F32 && part_o.dtype != q.dtype)) return NABLA_ERR_INVALID_ARG;
+  }
+  // outputs over inputs: refused, but for the merge in place
+  const char* o0 = static_cast<const char*>(o.ptr);
+  const char* o1 = heads_end(o, B, Sq, cache.D);
+  const int64_t pool = static_cast<int64_t>(cache.n_pages) * cache.H * cache.page * cache.D * 2;
+  const int64_t lse_bytes = static_cast<int64_t>(B) * q.H * Sq * 4;
+  auto hits = [](const void* a0, const void* a1, const void* b0, const void* b1) { return a0 < b1 && b0 < a1; };
+  auto end = [](const void* x, int64_t n) { return static_cast<const void*>(static_cast<const char*>(x) + n); };
+  if (heads_overlap(q, o, B, Sq, cache.D) || hits(o0, o1, cache.k, end(cache.k, pool)) ||
+      hits(o0, o1, cache.v, end(cache.v, pool)))
+    return NABLA_ERR_INVALID_ARG;
+  if (part) {
+    const bool same = part_o.ptr == o.ptr && part_o.dtype == o.dtype && part_o.stride_b == o.stride_b &&
+                      part_o.stride_h == o.stride_h && part_o.stride_s == o.stride_s;
+    if (!same && heads_overlap(part_o, o, B, Sq, cache.D)) return NABLA_ERR_INVALID_ARG;
+    if (hits(o0, o1, part_lse, end(part_lse, lse_bytes))) return NABLA_ERR_INVALID_ARG;
+  }
+  if (lse) {
+    const void* l1 = end(lse, lse_bytes);
+    if (hits(lse, l1, o0, o1) || hits(lse, l1, q.ptr, heads_end(q, B, Sq, cache.D)) ||
+        hits(lse, l1, cache.k, end(cache.k, pool)) || hits(lse, l1, cache.v, end(cache.v, pool)))
+      return NABLA_ERR_INVALID_ARG;
+    if (part && ((part_lse != lse && hits(lse, l1, part_lse, end(part_lse, lse_bytes))) ||
+                 hits(lse, l1, part_o.ptr, heads_end(part_o, B, Sq, cache.D))))
+      return NABLA_ERR_INVALID_ARG;
+  }
+  const int G = q.H / cache.H;
+  const Plan plan = make_plan(B, cache.H, G, Sq, cache.D);
+  if (!workspace || workspace_bytes < plan.bytes || (reinterpret_cast<uintptr_t>(workspace) & 255))
+    return NABLA_ERR_WORKSPACE;
+  AttnParams p = {};
+  p.q = q.ptr;
+  p.q_b = q.stride_b; p.q_h = q.stride_h; p.q_s = q.stride_s;
+  p.o = o.ptr;
+  p.o_b = o.stride_b; p.o_h = o.stride_h; p.o_s = o.stride_s;
+  p.o_f32 = o.dtype == NABLA_F32;
+  p.lse = lse;
+  if (part) {
+    p.part_o = part_o.ptr;
+    p.po_b = part_o.stride_b; p.po_h = part_o.stride_h; p.po_s = part_o.stride_s;
+    p.part_f32 = part_o.dtype == NABLA_F32;
+    p.part_lse = part_lse;
+  }
+  p.B = B; p.Hq = q.H; p.Hkv = cache.H; p.G = G; p.Sq = Sq; p.R = Sq * G;
+  p.div_r.init(p.R);
+  p.div_g.init(G);
+  p.prefix_pages = prefix_pages;
+  p.tail_pages = tail_pages;
+  p.tail_len = tail_len;
+  p.q_len = q_len;
+  p.P = prefix_len;
+  p.tail_width = tail_pages ? tail_width : 0;
+  p.page = cache.page;
+  while ((1 << p.page_shift) < cache.page) ++p.page_shift;
+  p.n_pages = cache.n_pages;
+  p.causal = causal;
+  p.scale_log2 = scale * 1.4426950408889634f;
+  p.shared = plan.shared;
+  p.n_rt = static_cast<int>(plan.n_rt);
+  // without tails (or without a prefix) shared mode has only the other kind of items
+  p.n_prefix = plan.shared && (prefix_len > 0 || !tail_pages) ? static_cast<int>(plan.n_prefix) : 0;
+  p.n_items = plan.shared ? p.n_prefix + (tail_pages ? static_cast<int>(plan.n_tail) : 0) : static_cast<int>(plan.n_items);
+  p.tail_half = p.R < 128 ? p.R : 128;
+  char* ws = static_cast<char*>(workspace);
+  p.cta_status = reinterpret_cast<uint32_t*>(ws + kStatusBytes);
+  p.cta_done = reinterpret_cast<int32_t*>(ws + kStatusBytes + 1024);
+  p.first = reinterpret_cast<int32_t*>(ws + plan.off_first);
+  p.last = reinterpret_cast<int32_t*>(ws + plan.off_last);
+  p.part_l = reinterpret_cast<float*>(ws + plan.off_l);
+  p.part_acc = reinterpret_cast<float*>(ws + plan.off_acc);
+  p.tail_base = plan.prefix_rows;
+  uint32_t* status = static_cast<uint32_t*>(workspace);
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  if (cache.D == 64)
+    return cache.dtype == NABLA_F16 ? launch<64, true>(p, cache, status, st) : launch<64, false>(p, cache, status, st);
+  return cache.dtype == NABLA_F16 ? launch<128, true>(p, cache, status, st) : launch<128, false>(p, cache, status, st);
+}

@@ -288,8 +288,8 @@ nabla_status nabla_read_device_status(void *workspace, uint32_t *code,
  * Continuing a clip from a history (no counterpart in the NABLA pages)
  * A long clip is generated in chunks of frames, often several candidates from one
  * history.  The sparse attention above covers a chunk's own tokens; the calls below give
- * Q and K their positions and keep the keys and values of finished frames in a paged
- * cache.  Conventions differ from the calls above only as stated: any
+ * Q and K their positions, keep the keys and values of finished frames in a paged cache
+ * and attend to them.  Conventions differ from the calls above only as stated: any
  * number of tokens, tensors as strided views, keys and values with fewer heads than the
  * queries (grouped heads).
  * --------------------------------------------------------------------------------- */
@@ -398,6 +398,46 @@ nabla_status nabla_cache_append(nabla_heads k, nabla_heads v, nabla_heads q_src,
                                 int32_t table_width, const int32_t *start, const int32_t *counts,
                                 const nabla_rope *rope, nabla_grid frame, int64_t pos0,
                                 const int32_t *positions, uint32_t *status, nabla_stream_t stream);
+
+/* Attention of B sequences over a prefix that all of them share and over each sequence's own
+ * tail, both in the paged cache.  With few query rows per sequence the rows of all sequences
+ * walk the prefix together, so its keys and values are read once for the batch.
+ *   s_ij = scale * q_i . k_j over the visible keys j (prefix first, then the tail),
+ *   O_i = sum_j softmax_j(s_ij) v_j,  LSE_i = ln sum_j exp(s_ij);  no visible key: O = 0,
+ *   LSE = -inf.
+ * q          : [B, Hq, Sq, D], Hq a multiple of cache.H; the cache's dtype.  Query head h reads
+ *              key head h / (Hq / cache.H).
+ * prefix_pages: int32 [ceil(prefix_len / page)] (nullable when prefix_len == 0).
+ * prefix_len : tokens of the shared prefix, >= 0 (host value).
+ * tail_pages : nullable int32 [B, tail_width]; tail_len: int32 [B] on the device, required with
+ *              it.  tail_width * page < 2^31.  Table entries past a tail's last page are not read.
+ * q_len      : nullable int32 [B] on the device: queries of each sequence (the first q_len[b]
+ *              of Sq; NULL = all).  Rows behind them are neither computed nor written.
+ * causal     : 0: a query sees its sequence's prefix and whole tail.  1: the queries are the
+ *              sequence's last tokens: query i of q_len[b] sees the keys j <= prefix_len +
+ *              tail_len[b] - q_len[b] + i.
+ * part_o,
+ * part_lse   : nullable partial result over other keys, merged into the output: part_o
+ *              [B, Hq, Sq, D] (f32, or q's dtype) and part_lse f32 [B, Hq, Sq], as
+ *              nabla_attn_fwd writes them (a row with part_lse = -inf has no part, whatever
+ *              part_o holds there).
+ * o          : out [B, Hq, Sq, D], q's dtype or f32.  lse: out, nullable f32 [B, Hq, Sq],
+ *              natural log.  Neither may overlap an input, except that o may be part_o and
+ *              lse part_lse (same address, dtype and strides).
+ * Keys and values of cache slots past a sequence's length may hold anything.  The
+ * probabilities enter the second product in the cache's 16-bit type; sums and statistics are
+ * f32.  Deterministic: no atomics on data.
+ * workspace  : >= nabla_prefix_workspace_bytes(B, Hq, cache.H, Sq, D) bytes, 256-byte
+ *              aligned; word 0 receives the device status (0x1xx, 0x301, 0x302; the rows of the
+ *              sequences concerned are unspecified).
+ * Errors: INVALID_ARG, UNSUPPORTED, WORKSPACE, CUDA. */
+size_t nabla_prefix_workspace_bytes(int32_t B, int32_t Hq, int32_t Hkv, int32_t Sq, int32_t D);
+nabla_status nabla_prefix_attn(nabla_heads q, int32_t B, int32_t Sq, nabla_cache cache,
+                               const int32_t *prefix_pages, int32_t prefix_len,
+                               const int32_t *tail_pages, int32_t tail_width, const int32_t *tail_len,
+                               const int32_t *q_len, int32_t causal, float scale, nabla_heads part_o,
+                               const float *part_lse, nabla_heads o, float *lse, void *workspace,
+                               size_t workspace_bytes, nabla_stream_t stream);
 
 #ifdef __cplusplus
 }
