@@ -49,6 +49,7 @@ constexpr int kMaxCtas = 148;
 constexpr int kKeys = 128;                // keys per tile
 constexpr int kRows = 256;                // query rows per item
 constexpr int kLaunchRegs = 168;
+constexpr int kPolyPairs = 2;             // of 8 pairs of weights, by poly_exp2
 constexpr int kRegProducer = 56;
 constexpr int kRegSoftmax = 224;
 static_assert(128 * kRegProducer + 256 * kRegSoftmax <= kThreads * kLaunchRegs,
@@ -173,9 +174,12 @@ __device__ __forceinline__ Item item_of(const AttnParams& p, int i) {
   }
   return t;
 }
-__device__ __forceinline__ int units_of(const Item& t) { return max(t.np + t.nt, 1); }
+__device__ __forceinline__ int length_of(const Item& t) { return max(t.np + t.nt, 1); }
 
-// A CTA's share of the work, part by part: key tiles [x0, x1) of an item.
+// A CTA's share of the work, part by part: key tiles [x0, x1) of an item.  An item counts as
+// its tiles and kSetup more (its Q, its pipeline's fill and its epilogue); a run that ends
+// inside an item's setup leaves the item to the next CTA.
+constexpr int kSetup = 2;
 struct Walk {
   int round, item, x0;
   long long left;
@@ -191,17 +195,19 @@ struct Walk {
       ++round;
       o->t = item_of(p, o->i);
       o->x0 = 0;
-      o->x1 = o->total = units_of(o->t);
+      o->x1 = o->total = length_of(o->t);
     } else {
       if (left <= 0) return false;
       o->i = item;
       o->t = item_of(p, item);
-      o->total = units_of(o->t);
-      o->x0 = x0;
-      o->x1 = static_cast<int>(min(static_cast<long long>(o->total), x0 + left));
-      left -= o->x1 - o->x0;
+      o->total = length_of(o->t);
+      const long long end = min(static_cast<long long>(o->total + kSetup), x0 + left);
+      o->x0 = max(x0 - kSetup, 0);
+      o->x1 = max(static_cast<int>(end) - kSetup, 0);
+      left -= end - x0;
       ++item;
       x0 = 0;
+      if (o->x1 == 0) return false;
     }
     o->n = o->t.np + o->t.nt == 0 ? 0 : o->x1 - o->x0;
     return true;
@@ -225,14 +231,33 @@ template <int D>
 struct Cfg {
   static constexpr int kPanels = D / 64;
   static constexpr int kTileBytes = 128 * D * 2;
-  static constexpr int kStages = D == 128 ? 5 : 8;
+  static constexpr int kStages = D == 128 ? 4 : 8;
   static constexpr int kOffKv = 2 * kTileBytes;
-  static constexpr int kOffBar = kOffKv + kStages * kTileBytes;
+  static constexpr int kOffOut = kOffKv + kStages * kTileBytes;    // 8 warps x 32 rows x 128 bytes
+  static constexpr int kOffBar = kOffOut + 8 * 4096;
   static constexpr int kSmemBytes = kOffBar + 1024 + static_cast<int>(sizeof(Bars));
   static_assert(kSmemBytes <= 232448, "shared memory");
   static __device__ __forceinline__ uint32_t col_s(int s) { return s * 128u; }
   static __device__ __forceinline__ uint32_t col_o(int s) { return 256u + s * 128u; }
 };
+
+// mbar_wait() for short hand-overs: probes without reading the timer, which is looked at (and
+// the limit applied) every 256 probes only.
+__device__ __forceinline__ bool bar_wait(uint64_t* bar, uint32_t parity, uint32_t* status, uint32_t code) {
+  uint64_t t0 = 0;
+  for (uint32_t i = 1; !mbar_try_wait(bar, parity); ++i) {
+    if ((i & 255u) == 0u) {
+      const uint64_t t = global_timer_ns();
+      if (t0 == 0) t0 = t;
+      if (t - t0 > kWaitLimitNs) {
+        record_status(status, code);
+        return false;
+      }
+      if (*reinterpret_cast<volatile uint32_t*>(status) != 0u) return false;
+    }
+  }
+  return true;
+}
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
@@ -243,6 +268,26 @@ __device__ __forceinline__ long long part_row(const AttnParams& p, int i, int ct
   if (!p.shared) return (static_cast<long long>(2 * cta + (cont ? 0 : 1)) * 2 + half) * 128 + row;
   if (i < p.n_prefix) return (static_cast<long long>(i + cta) * 2 + half) * 128 + row;
   return p.tail_base + (static_cast<long long>(i - p.n_prefix + cta) * 2 + half) * p.tail_half + row;
+}
+
+// 2^y for a pair of arguments, without the special-function unit: y = n + f with n
+// whole and |f| <= 1/2 (adding 1.5 * 2^23 leaves n in the low mantissa bits), 2^f by the
+// minimax polynomial of degree 4 (Remez exchange on [-1/2, 1/2], relative error below
+// 2.6e-6), and n added to the exponent.  Results end at 2^-126 and 2^127 (a NaN gives one
+// of them).
+__device__ __forceinline__ float2 poly_exp2(float2 y) {
+  const float2 magic = make_float2(12582912.f, 12582912.f), back = make_float2(-12582912.f, -12582912.f);
+  y.x = fminf(fmaxf(y.x, -126.f), 127.f);
+  y.y = fminf(fmaxf(y.y, -126.f), 127.f);
+  const float2 t = __fadd2_rn(y, magic);
+  const float2 n = __fadd2_rn(t, back);
+  const float2 f = __ffma2_rn(n, make_float2(-1.f, -1.f), y);
+  float2 r = __ffma2_rn(make_float2(0.0095701021f, 0.0095701021f), f, make_float2(0.0559178591f, 0.0559178591f));
+  r = __ffma2_rn(r, f, make_float2(0.2402474433f, 0.2402474433f));
+  r = __ffma2_rn(r, f, make_float2(0.6931217909f, 0.6931217909f));
+  r = __ffma2_rn(r, f, make_float2(0.9999992847f, 0.9999992847f));
+  return make_float2(__uint_as_float(__float_as_uint(r.x) + (__float_as_uint(t.x) << 23)),
+                     __uint_as_float(__float_as_uint(r.y) + (__float_as_uint(t.y) << 23)));
 }
 
 // log2(2^a + 2^b)
@@ -287,9 +332,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(&B.q_empty, 1);
     for (int s = 0; s < 2; ++s) {
       mbar_init(&B.s_full[s], 1);
-      mbar_init(&B.p_full[s], 128);
+      mbar_init(&B.p_full[s], 4);
       mbar_init(&B.o_done[s], 1);
-      mbar_init(&B.o_free[s], 128);
+      mbar_init(&B.o_free[s], 4);
     }
     mbar_init(&B.drain, 1);
     fence_mbarrier_init();
@@ -308,7 +353,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int per = (n + kThreads - 1) / kThreads;
     const int a = min(static_cast<int>(threadIdx.x) * per, n), b = min(a + per, n);
     int sum = 0;
-    for (int i = a; i < b; ++i) sum += units_of(item_of(p, i0 + i));
+    for (int i = a; i < b; ++i) sum += length_of(item_of(p, i0 + i)) + kSetup;
     int inc = sum;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -330,7 +375,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (u1 > u0 && u0 >= at && u0 < at + sum) {
       int i = a, len = 0;
       for (; i < b; ++i) {
-        len = units_of(item_of(p, i0 + i));
+        len = length_of(item_of(p, i0 + i)) + kSetup;
         if (u0 < at + len) break;
         at += len;
       }
@@ -362,11 +407,30 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       const int rows_pp = min(p.page, kKeys);            // rows per piece
       const int piece = lane / C::kPanels, panel = lane % C::kPanels;
-      long long g = 0;          // stages filled
-      long long n_part = 0;     // partial V tiles
+      uint32_t g = 0;           // stages filled
+      // A partial V tile's missing rows are zeroed once it has landed, and only then is it
+      // handed on; the next K is requested first.
+      uint32_t n_cut = 0;       // partial V tiles
+      int cut_stage = -1, cut_valid = 0;
       bool ok = true;
       auto wait_all = [&](uint64_t* bar, uint32_t parity, uint32_t code) -> bool {
-        return __all_sync(0xffffffffu, mbar_wait(bar, parity, status, code));
+        return __all_sync(0xffffffffu, bar_wait(bar, parity, status, code));
+      };
+      auto finish_cut = [&]() -> bool {
+        if (cut_stage < 0) return true;
+        if (!wait_all(&B.v_part, n_cut & 1, kDevTimeoutTmaFull)) return false;
+        ++n_cut;
+        unsigned char* dst = sKV + cut_stage * C::kTileBytes;
+        for (int e = cut_valid * 8 + lane; e < kKeys * 8; e += 32)
+#pragma unroll
+          for (int pn = 0; pn < C::kPanels; ++pn)
+            *reinterpret_cast<uint4*>(dst + pn * 16384 + e * 16) = make_uint4(0u, 0u, 0u, 0u);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&B.full[cut_stage]);
+        __syncwarp();
+        cut_stage = -1;
+        return true;
       };
       while (ok && walk.next(p, &part)) {
         const int L = part.t.b >= 0 ? tail_of(p, part.t.b) : 0;
@@ -395,7 +459,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (x + 1 < xe) id = lookup(x + 1);
 #pragma unroll
           for (int kv = 0; kv < 2; ++kv) {
-            const int st = static_cast<int>(g % C::kStages);
+            const uint32_t st = g % C::kStages;
             if (g >= C::kStages &&
                 !wait_all(&B.empty[st], (g / C::kStages - 1) & 1, kDevTimeoutKvEmpty)) {
               ok = false;
@@ -410,90 +474,90 @@ __global__ void __launch_bounds__(kThreads, 1)
               tma_load_4d(dst + panel * 16384 + piece * rows_pp * 128, kv ? &map_v : &map_k, bar, panel * 64, slot,
                           part.t.kvh, cur);
             __syncwarp();
-            if (cut) {
-              if (!wait_all(&B.v_part, n_part & 1, kDevTimeoutTmaFull)) {
+            if (kv == 0) {
+              if (!finish_cut()) {
                 ok = false;
                 break;
               }
-              ++n_part;
-              for (int e = valid * 8 + lane; e < kKeys * 8; e += 32)
-#pragma unroll
-                for (int pn = 0; pn < C::kPanels; ++pn)
-                  *reinterpret_cast<uint4*>(dst + pn * 16384 + e * 16) = make_uint4(0u, 0u, 0u, 0u);
-              fence_proxy_async_smem();
-              __syncwarp();
-              if (lane == 0) mbar_arrive(&B.full[st]);
-              __syncwarp();
+            } else if (cut) {
+              cut_stage = static_cast<int>(st);
+              cut_valid = valid;
             }
             ++g;
           }
         }
       }
+      if (ok) ok = finish_cut();
+      if (!ok && cut_stage >= 0) bar_wait(&B.v_part, n_cut & 1, status, kDevTimeoutDrain);
       // Copies still in flight must land before the CTA exits.
-      for (long long x = g > C::kStages ? g - C::kStages : 0; x < g; ++x)
-        mbar_wait(&B.full[x % C::kStages], (x / C::kStages) & 1, status, kDevTimeoutDrain);
+      for (uint32_t x = g > C::kStages ? g - C::kStages : 0; x < g; ++x)
+        bar_wait(&B.full[x % C::kStages], (x / C::kStages) & 1, status, kDevTimeoutDrain);
       __syncwarp();
     } else if (warp == 1) {
       // ------------------------------------------------------------------ MMA issuer
-      if (lane == 0) {
+      // One elected lane.  (elect.sync, not a lane comparison: the compiler then keeps
+      // descriptors in uniform registers, and eight MMAs issue back to back.)
+      if (elect_one()) {
         constexpr uint32_t idesc_s = F16 ? idesc_f16_f32(128, 128, false, false) : idesc_bf16_f32(128, 128, false, false);
         constexpr uint32_t idesc_o = F16 ? idesc_f16_f32(128, D, false, true) : idesc_bf16_f32(128, D, false, true);
-        const uint32_t q_addr = smem_u32(smem), kv_addr = smem_u32(sKV);
-        long long g0 = 0;               // stages of earlier parts
-        long long n_q = 0;              // parts with keys
-        long long n_p[2] = {0, 0};      // P V issued per slot
-        long long n_o[2] = {0, 0};      // parts finished per slot
+        constexpr uint32_t kTile16 = C::kTileBytes >> 4;       // descriptors count 16 bytes
+        const uint64_t desc_q = sdesc_sw128(smem_u32(smem), 16, 1024);
+        const uint64_t desc_k = sdesc_sw128(smem_u32(sKV), 16, 1024);
+        const uint64_t desc_v = sdesc_sw128(smem_u32(sKV), 16384, 1024);
+        uint32_t g0 = 0;                // stages of earlier parts
+        uint32_t n_q = 0;               // parts with keys
+        uint32_t n_p0 = 0, n_p1 = 0;    // P V issued per slot
+        uint32_t n_o0 = 0, n_o1 = 0;    // parts finished per slot
         bool ok = true;
-        auto full = [&](long long g) -> bool {
-          return mbar_wait(&B.full[g % C::kStages], (g / C::kStages) & 1, status, kDevTimeoutTmaFull);
+        auto full = [&](uint32_t g) -> bool {
+          return bar_wait(&B.full[g % C::kStages], (g / C::kStages) & 1, status, kDevTimeoutTmaFull);
         };
         while (ok && walk.next(p, &part)) {
           if (part.n == 0) continue;
           const int dual = part.t.dual ? 1 : 0;
           const int steps = part.n << dual;
-          if (!mbar_wait(&B.q_full, n_q & 1, status, kDevTimeoutQFull)) break;
+          if (!bar_wait(&B.q_full, n_q & 1, status, kDevTimeoutQFull)) break;
           ++n_q;
           for (int t = 0; t < steps + 2; ++t) {
-            const int s = t & 1;
+            const uint32_t s = t & 1;
             if (t >= 2) {
               // O += P V of step t - 2 (same slot)
-              const int x = (t - 2) >> dual;
-              const long long gv = g0 + 2 * x + 1;
+              const uint32_t x = static_cast<uint32_t>(t - 2) >> dual;
+              const uint32_t gv = g0 + 2 * x + 1;
               const bool first = dual ? x == 0 : x < 2;
-              if (!mbar_wait(&B.p_full[s], n_p[s] & 1, status, kDevTimeoutPFull) || !full(gv) ||
-                  (first && n_o[s] > 0 && !mbar_wait(&B.o_free[s], (n_o[s] - 1) & 1, status, kDevTimeoutOBar))) {
+              const uint32_t n_p = s ? n_p1 : n_p0, n_o = s ? n_o1 : n_o0;
+              if (!bar_wait(&B.p_full[s], n_p & 1, status, kDevTimeoutPFull) || !full(gv) ||
+                  (first && n_o > 0 && !bar_wait(&B.o_free[s], (n_o - 1) & 1, status, kDevTimeoutOBar))) {
                 ok = false;
                 break;
               }
-              ++n_p[s];
+              if (s) ++n_p1; else ++n_p0;
               tc_fence_after();
-              const uint32_t v = kv_addr + static_cast<uint32_t>(gv % C::kStages) * C::kTileBytes;
+              const uint64_t v = desc_v + gv % C::kStages * kTile16;
+              const uint32_t o_t = tmem + C::col_o(s), p_t = tmem + C::col_s(s);
 #pragma unroll
-              for (int kk = 0; kk < kKeys / 16; ++kk) {
-                const uint64_t bd = sdesc_sw128(v + kk * 2048, 16384, 1024);
-                mma_bf16_ts(tmem + C::col_o(s), tmem + C::col_s(s) + kk * 8, bd, idesc_o, (!first || kk > 0) ? 1u : 0u);
-              }
+              for (int kk = 0; kk < kKeys / 16; ++kk)
+                mma_bf16_ts(o_t, p_t + kk * 8, v + kk * (2048 >> 4), idesc_o, (!first || kk > 0) ? 1u : 0u);
               if (!dual || s == 1) mma_commit(&B.empty[gv % C::kStages]);
               if (t >= steps) {          // the slot's last step
                 mma_commit(&B.o_done[s]);
-                ++n_o[s];
+                if (s) ++n_o1; else ++n_o0;
               }
             }
             if (t < steps) {
-              const int x = t >> dual;
-              const long long gk = g0 + 2 * x;
+              const uint32_t gk = g0 + 2 * (static_cast<uint32_t>(t) >> dual);
               if (!full(gk)) {
                 ok = false;
                 break;
               }
               tc_fence_after();
-              const uint32_t qs = q_addr + (dual ? s : 0) * C::kTileBytes;
-              const uint32_t k = kv_addr + static_cast<uint32_t>(gk % C::kStages) * C::kTileBytes;
+              const uint64_t qd = desc_q + (dual ? s : 0u) * kTile16;
+              const uint64_t kd = desc_k + gk % C::kStages * kTile16;
+              const uint32_t s_t = tmem + C::col_s(s);
 #pragma unroll
               for (int kk = 0; kk < D / 16; ++kk) {
-                const uint32_t off = (kk >> 2) * 16384 + (kk & 3) * 32;
-                mma_bf16_ss(tmem + C::col_s(s), sdesc_sw128(qs + off, 16, 1024), sdesc_sw128(k + off, 16, 1024), idesc_s,
-                            kk > 0 ? 1u : 0u);
+                const uint32_t off = ((kk >> 2) * 16384 + (kk & 3) * 32) >> 4;
+                mma_bf16_ss(s_t, qd + off, kd + off, idesc_s, kk > 0 ? 1u : 0u);
               }
               mma_commit(&B.s_full[s]);
               if (!dual || s == 1) mma_commit(&B.empty[gk % C::kStages]);
@@ -503,7 +567,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           g0 += 2 * part.n;
         }
         mma_commit(&B.drain);
-        mbar_wait(&B.drain, 0, status, kDevTimeoutDrain);
+        bar_wait(&B.drain, 0, status, kDevTimeoutDrain);
       }
       __syncwarp();
     } else {
@@ -515,14 +579,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int c = tid % kChunks, r_first = tid / kChunks;
       constexpr int kStep = 64 / kChunks;
       const uint16_t* q = static_cast<const uint16_t*>(p.q);
-      long long n_q = 0;
+      uint32_t n_q = 0;
       bool ok = true;
       while (ok && walk.next(p, &part)) {
         if (part.n == 0) continue;
         const int n_rows = part.t.dual ? 256 : 128;
-        if (n_q > 0) ok = __all_sync(0xffffffffu, mbar_wait(&B.q_empty, (n_q - 1) & 1, status, kDevTimeoutQFull));
+        if (n_q > 0) ok = __all_sync(0xffffffffu, bar_wait(&B.q_empty, (n_q - 1) & 1, status, kDevTimeoutQFull));
         if (!ok) break;
         ++n_q;
+#pragma unroll 4
         for (int r = r_first; r < n_rows; r += kStep) {
           unsigned char* dst = smem + (r >> 7) * C::kTileBytes + (c >> 3) * 16384 + (r & 127) * 128 +
                                (((c & 7) ^ (r & 7)) << 4);
@@ -555,7 +620,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // range allows, so that weights down to 2^-31 of it are kept (2^-24 without the bias; a
     // long prefix has enough small ones to matter).
     constexpr float kBias = F16 ? 7.0f : 0.0f;
-    long long n_s = 0, n_o = 0;
+    uint32_t n_s = 0, n_o = 0;
     bool ok = true;
     while (ok && walk.next(p, &part)) {
       // the row: its sequence, query and head, and the keys it sees
@@ -582,74 +647,112 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool any = false;
       for (int x = x_first; x < xe; x += stride) {
         any = true;
-        ok = __all_sync(0xffffffffu, mbar_wait(&B.s_full[slot], n_s & 1, status, kDevTimeoutSFull));
+        ok = __all_sync(0xffffffffu, bar_wait(&B.s_full[slot], n_s & 1, status, kDevTimeoutSFull));
         if (!ok) break;
         tc_fence_after();
-        uint32_t sv[128];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) tmem_ld32(s_col + 32 * i, *reinterpret_cast<uint32_t(*)[32]>(&sv[32 * i]));
-        tmem_wait_ld();
-#pragma unroll
-        for (int i = 0; i < 4; ++i) reg_fence32(*reinterpret_cast<uint32_t(*)[32]>(&sv[32 * i]));
         const int seen = x < part.t.np ? lim_p - x * kKeys : lim_t - (x - part.t.np) * kKeys;
-        if (__any_sync(0xffffffffu, seen < kKeys)) {
-#pragma unroll
-          for (int i = 0; i < 128; ++i) sv[i] = i < seen ? sv[i] : 0xFF800000u;
-        }
-        float m8[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) m8[i] = -INFINITY;
-#pragma unroll
-        for (int i = 0; i < 128; i += 2)
-          m8[(i >> 1) & 7] = fmax3(m8[(i >> 1) & 7], __uint_as_float(sv[i]), __uint_as_float(sv[i + 1]));
-        const float mx = fmaxf(fmaxf(fmaxf(m8[0], m8[1]), fmaxf(m8[2], m8[3])),
-                               fmaxf(fmaxf(m8[4], m8[5]), fmaxf(m8[6], m8[7])));
-        float factor = 1.f;
-        bool rescale = false;
-        const float rm = mx * sl2 - kBias;
-        if (mx != -INFINITY && rm > m_ref + 8.0f) {
-          if (m_ref != -INFINITY) {
-            factor = fast_exp2(m_ref - rm);
-            rescale = true;
-          }
-          m_ref = rm;
-        }
-        const float neg = m_ref == -INFINITY ? 0.f : -m_ref;
-        const float2 negv = make_float2(neg, neg);
         float2 acc = make_float2(0.f, 0.f);
+        bool done = false;
+        if (__all_sync(0xffffffffu, seen >= kKeys && m_ref != -INFINITY)) {
+          // Usual tile: weights against the reference of the tiles before, 32 keys at a time as
+          // they arrive, some of the exponentials on the FMA pipe.  Their sum decides whether
+          // the reference still holds: up to 2^15 no weight is too large (for fp16 either),
+          // and NaN or infinity fails; the scores are intact until then.
+          const float2 negv = make_float2(-m_ref, -m_ref);
+          uint32_t buf[2][32], pk[64];       // scores; weights as 16-bit pairs
+          tmem_ld32(s_col, buf[0]);
 #pragma unroll
-        for (int e = 0; e < 64; ++e) {
-          const float2 y = __ffma2_rn(make_float2(__uint_as_float(sv[2 * e]), __uint_as_float(sv[2 * e + 1])), sl2v, negv);
-          const float2 pr = make_float2(fast_exp2(y.x), fast_exp2(y.y));
-          acc = __fadd2_rn(acc, pr);
-          sv[e] = pack2<F16>(pr.x, pr.y);
-        }
-        tmem_st32(s_col, *reinterpret_cast<uint32_t(*)[32]>(&sv[0]));
-        tmem_st32(s_col + 32, *reinterpret_cast<uint32_t(*)[32]>(&sv[32]));
-        // Every earlier P V of the slot was issued before this S, so its completion covers
-        // them: the accumulator may be rescaled at once.
-        if (__any_sync(0xffffffffu, rescale)) {
-#pragma unroll 1
-          for (int o0 = 0; o0 < D; o0 += 16) {
-            uint32_t ov[16];
-            tmem_ld16(o_col + o0, ov);
+          for (int c = 0; c < 4; ++c) {
             tmem_wait_ld();
-            reg_fence16(ov);
+            reg_fence32(buf[c & 1]);
+            if (c < 3) tmem_ld32(s_col + 32 * (c + 1), buf[(c + 1) & 1]);
 #pragma unroll
-            for (int i = 0; i < 16; ++i) ov[i] = __float_as_uint(__uint_as_float(ov[i]) * factor);
-            tmem_st16(o_col + o0, ov);
+            for (int e = 0; e < 16; ++e) {
+              const float2 z = make_float2(__uint_as_float(buf[c & 1][2 * e]), __uint_as_float(buf[c & 1][2 * e + 1]));
+              const float2 y = __ffma2_rn(z, sl2v, negv);
+              const float2 pr = (e & 7) < kPolyPairs ? poly_exp2(y) : make_float2(fast_exp2(y.x), fast_exp2(y.y));
+              acc = __fadd2_rn(acc, pr);
+              pk[16 * c + e] = pack2<F16>(pr.x, pr.y);
+            }
+          }
+          done = __all_sync(0xffffffffu, acc.x + acc.y <= 32768.f);
+          if (done) {
+            l += acc.x + acc.y;
+            tmem_st32(s_col, *reinterpret_cast<uint32_t(*)[32]>(&pk[0]));
+            tmem_st32(s_col + 32, *reinterpret_cast<uint32_t(*)[32]>(&pk[32]));
           }
         }
-        l = l * factor + (acc.x + acc.y);
+        if (!done) {
+          // First tile, a masked one, or a maximum that has grown: one pass over the scores
+          // for the maximum, one for the weights.
+          float mx = -INFINITY;
+#pragma unroll 1
+          for (int c = 0; c < 4; ++c) {
+            uint32_t sv[32];
+            tmem_ld32(s_col + 32 * c, sv);
+            tmem_wait_ld();
+            reg_fence32(sv);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) mx = fmaxf(mx, 32 * c + i < seen ? __uint_as_float(sv[i]) : -INFINITY);
+          }
+          float factor = 1.f;
+          bool rescale = false;
+          const float rm = mx * sl2 - kBias;
+          if (mx != -INFINITY && rm > m_ref + 8.0f) {
+            if (m_ref != -INFINITY) {
+              factor = fast_exp2(m_ref - rm);
+              rescale = true;
+            }
+            m_ref = rm;
+          }
+          const float neg = m_ref == -INFINITY ? 0.f : -m_ref;
+          const float2 negv = make_float2(neg, neg);
+          acc = make_float2(0.f, 0.f);
+#pragma unroll 1
+          for (int c = 0; c < 4; ++c) {
+            // the weights of keys 32 c .. go to columns 16 c .., whose scores have been read
+            uint32_t sv[32], pk[16];
+            tmem_ld32(s_col + 32 * c, sv);
+            tmem_wait_ld();
+            reg_fence32(sv);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              const int i = 32 * c + 2 * e;
+              const float2 z = make_float2(i < seen ? __uint_as_float(sv[2 * e]) : -INFINITY,
+                                           i + 1 < seen ? __uint_as_float(sv[2 * e + 1]) : -INFINITY);
+              const float2 y = __ffma2_rn(z, sl2v, negv);
+              const float2 pr = make_float2(fast_exp2(y.x), fast_exp2(y.y));
+              acc = __fadd2_rn(acc, pr);
+              pk[e] = pack2<F16>(pr.x, pr.y);
+            }
+            tmem_st16(s_col + 16 * c, pk);
+          }
+          // Every earlier P V of the slot was issued before this S, so its completion covers
+          // them: the accumulator may be rescaled at once.
+          if (__any_sync(0xffffffffu, rescale)) {
+#pragma unroll 1
+            for (int o0 = 0; o0 < D; o0 += 16) {
+              uint32_t ov[16];
+              tmem_ld16(o_col + o0, ov);
+              tmem_wait_ld();
+              reg_fence16(ov);
+#pragma unroll
+              for (int i = 0; i < 16; ++i) ov[i] = __float_as_uint(__uint_as_float(ov[i]) * factor);
+              tmem_st16(o_col + o0, ov);
+            }
+          }
+          l = l * factor + (acc.x + acc.y);
+        }
         tmem_wait_st();
         tc_fence_before();
-        mbar_arrive(&B.p_full[slot]);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&B.p_full[slot]);
         ++n_s;
       }
       if (!ok) break;
       // ------------------------------------------------------------------ the part's result
       if (any) {
-        ok = __all_sync(0xffffffffu, mbar_wait(&B.o_done[slot], n_o & 1, status, kDevTimeoutOBar));
+        ok = __all_sync(0xffffffffu, bar_wait(&B.o_done[slot], n_o & 1, status, kDevTimeoutOBar));
         if (!ok) break;
         ++n_o;
         tc_fence_after();
@@ -658,15 +761,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       float inv = l == 0.f ? 0.f : 1.f / l;
       float sum2 = l == 0.f ? -INFINITY : m_ref + log2f(l);
       const bool whole = !p.shared && part.x0 == 0 && part.x1 == part.total;
-      const float* prow = nullptr;
-      const uint16_t* prow16 = nullptr;
+      // where the row goes: bit 0 of `how` = written, bit 1 = merged with the caller's part
+      long long at = 0, part_at = 0;
       float pw = 0.f;
-      float* wrow = nullptr;
-      unsigned char* orow = nullptr;
+      int how = 0;
       if (whole) {
         if (valid) {
           const int h = part.t.kvh * p.G + gh;
           const long long flat = (static_cast<long long>(b) * p.Hq + h) * p.Sq + s;
+          how = 1;
           if (p.part_lse != nullptr) {
             const float a = p.part_lse[flat] * 1.4426950408889634f;
             if (a != -INFINITY) {
@@ -674,13 +777,12 @@ __global__ void __launch_bounds__(kThreads, 1)
               inv *= sum2 == -INFINITY ? 0.f : exp2f(sum2 - both);
               pw = exp2f(a - both);
               sum2 = both;
-              const long long off = b * p.po_b + h * p.po_h + s * p.po_s;
-              if (p.part_f32) prow = static_cast<const float*>(p.part_o) + off;
-              else prow16 = static_cast<const uint16_t*>(p.part_o) + off;
+              part_at = b * p.po_b + h * p.po_h + s * p.po_s;
+              how = 3;
             }
           }
           if (p.lse != nullptr) p.lse[flat] = sum2 * 0.69314718055994531f;
-          orow = static_cast<unsigned char*>(p.o) + (b * p.o_b + h * p.o_h + s * p.o_s) * (p.o_f32 ? 4 : 2);
+          at = b * p.o_b + h * p.o_h + s * p.o_s;
         }
       } else {
         if (part.x0 == 0 && threadIdx.x == kSoftmaxWarp0 * 32) p.first[part.i - p.whole * gridDim.x] = blockIdx.x;
@@ -691,57 +793,82 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (valid) {
           const long long w = part_row(p, part.i, blockIdx.x, part.x0 > 0, slot, row);
           p.part_l[w] = sum2;
-          if (sum2 != -INFINITY) wrow = p.part_acc + w * D;
+          how = sum2 != -INFINITY ? 1 : 0;
+          at = w * D;
         }
       }
-#pragma unroll 1
+      // 32 channels at a time the warp's 32 rows go through shared memory, so that a store
+      // covers whole 128-byte lines (8 lanes a row) instead of 16 bytes of 32 rows: 5 us
+      // less per item of 128 f32 rows.
+      const bool to_f32 = !whole || p.o_f32;
+      unsigned char* stage = smem + C::kOffOut + (warp - kSoftmaxWarp0) * 4096;
+      // the rows whose channels 4 ch .. 4 ch + 3 (of every 32) this lane stores
+      const int ch = lane & 7;
+      long long to[8];
+      uint32_t hows = 0;
+#pragma unroll
+      for (int it = 0; it < 8; ++it) {
+        const int rr = 4 * it + (lane >> 3);
+        to[it] = __shfl_sync(0xffffffffu, at, rr) + 4 * ch;
+        hows |= static_cast<uint32_t>(__shfl_sync(0xffffffffu, how, rr)) << (2 * it);
+      }
+      const bool merge = __any_sync(0xffffffffu, (how & 2) != 0);
+#pragma unroll
       for (int d0 = 0; d0 < D; d0 += 32) {
         uint32_t a[32];
         if (any) {
           tmem_ld32(o_col + d0, a);
           tmem_wait_ld();
           reg_fence32(a);
-        } else {
-#pragma unroll
-          for (int i = 0; i < 32; ++i) a[i] = 0u;
         }
         if (any && d0 + 32 == D) {
           tc_fence_before();
-          mbar_arrive(&B.o_free[slot]);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&B.o_free[slot]);
         }
-        float f[32];
+        if (!any || inv == 0.f) {
 #pragma unroll
-        for (int i = 0; i < 32; ++i) f[i] = inv == 0.f ? 0.f : __uint_as_float(a[i]) * inv;
-        if (prow != nullptr) {
+          for (int i = 0; i < 32; ++i) a[i] = 0u;
+        }
+        float4 y[8];
+        if (merge) {
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const float4 y = *reinterpret_cast<const float4*>(prow + d0 + 4 * i);
-            f[4 * i] += pw * y.x; f[4 * i + 1] += pw * y.y; f[4 * i + 2] += pw * y.z; f[4 * i + 3] += pw * y.w;
-          }
-        } else if (prow16 != nullptr) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const uint4 y = *reinterpret_cast<const uint4*>(prow16 + d0 + 8 * i);
-            const uint32_t w[4] = {y.x, y.y, y.z, y.w};
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const float2 z = unpack2<F16>(w[j]);
-              f[8 * i + 2 * j] += pw * z.x;
-              f[8 * i + 2 * j + 1] += pw * z.y;
+          for (int it = 0; it < 8; ++it) {
+            const long long from = __shfl_sync(0xffffffffu, part_at, 4 * it + (lane >> 3)) + 4 * ch + d0;
+            y[it] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (hows >> (2 * it) & 2) {
+              if (p.part_f32) {
+                y[it] = *reinterpret_cast<const float4*>(static_cast<const float*>(p.part_o) + from);
+              } else {
+                const uint2 v = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p.part_o) + from);
+                const float2 y0 = unpack2<F16>(v.x), y1 = unpack2<F16>(v.y);
+                y[it] = make_float4(y0.x, y0.y, y1.x, y1.y);
+              }
             }
           }
         }
-        float4* w4 = wrow != nullptr ? reinterpret_cast<float4*>(wrow + d0)
-                     : (orow != nullptr && p.o_f32) ? reinterpret_cast<float4*>(orow + d0 * 4) : nullptr;
-        if (w4 != nullptr) {
+        __syncwarp();
 #pragma unroll
-          for (int i = 0; i < 8; ++i) w4[i] = make_float4(f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3]);
-        } else if (orow != nullptr) {
-          uint4* o4 = reinterpret_cast<uint4*>(orow + d0 * 2);
+        for (int i = 0; i < 8; ++i)
+          *reinterpret_cast<float4*>(stage + lane * 128 + ((i ^ (lane & 7)) << 4)) =
+              make_float4(__uint_as_float(a[4 * i]) * inv, __uint_as_float(a[4 * i + 1]) * inv,
+                          __uint_as_float(a[4 * i + 2]) * inv, __uint_as_float(a[4 * i + 3]) * inv);
+        __syncwarp();
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            o4[i] = make_uint4(pack2<F16>(f[8 * i], f[8 * i + 1]), pack2<F16>(f[8 * i + 2], f[8 * i + 3]),
-                               pack2<F16>(f[8 * i + 4], f[8 * i + 5]), pack2<F16>(f[8 * i + 6], f[8 * i + 7]));
+        for (int it = 0; it < 8; ++it) {
+          const int rr = 4 * it + (lane >> 3);
+          float4 f = *reinterpret_cast<const float4*>(stage + rr * 128 + ((ch ^ (rr & 7)) << 4));
+          if (merge) {
+            const float w = __shfl_sync(0xffffffffu, pw, rr);
+            f.x += w * y[it].x; f.y += w * y[it].y; f.z += w * y[it].z; f.w += w * y[it].w;
+          }
+          if (hows >> (2 * it) & 1) {
+            if (to_f32)
+              *reinterpret_cast<float4*>((whole ? static_cast<float*>(p.o) : p.part_acc) + to[it] + d0) = f;
+            else
+              *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.o) + to[it] + d0) =
+                  make_uint2(pack2<F16>(f.x, f.y), pack2<F16>(f.z, f.w));
+          }
         }
       }
     }
@@ -755,14 +882,49 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-// Joins the parts of split items, one warp per row, in the order of their keys' CTAs
-// (deterministic), merges the caller's part and writes the row.  Block 0 also gathers the
-// CTAs' status words and looks the lengths over.
-constexpr int kJoinWarps = 8;
+// Joins the parts of split items, merges the caller's part and writes the rows; block 0
+// also gathers the CTAs' status words and looks the lengths over.  Four warps share a row: a
+// long prefix leaves a row up to two parts per CTA, which are read in parallel (every fourth
+// part by one warp, always the same ones, so results do not depend on timing).
+constexpr int kJoinThreads = 256;
+constexpr int kRowWarps = 4;
+constexpr int kJoinRows = kJoinThreads / 32 / kRowWarps;     // rows at a time
+constexpr int kJoinBlocks = 16;                              // blocks per split item (own mode)
+
+// Parts of one item that hold a row: the first in workspace row r0, part j > 0 in r1 +
+// (j - 1) step.
+struct PartList {
+  int n;
+  long long r0, r1;
+  int step;
+  __device__ __forceinline__ long long at(int j) const { return j == 0 ? r0 : r1 + static_cast<long long>(j - 1) * step; }
+};
+
+__device__ __forceinline__ PartList parts_of(const AttnParams& p, int i, int lrow, bool dual, int ctas) {
+  PartList l;
+  const int e = i - p.whole * ctas;
+  const int first = p.first[e], last = p.last[e];
+  l.n = 0;
+  if (first < 0 || last < first || last >= ctas) return l;       // only after a wait gave up
+  const int half = dual ? lrow >> 7 : 0, row = dual ? lrow & 127 : lrow;
+  l.r0 = part_row(p, i, first, false, half, row);
+  if (!p.shared) {
+    l.n = last - first + 1;
+    l.r1 = part_row(p, i, first + 1, true, half, row);
+    l.step = 4 * 128;
+  } else {
+    l.n = (last - first + 1) * (dual ? 1 : 2);
+    l.step = (i < p.n_prefix ? 128 : p.tail_half) * (dual ? 2 : 1);
+    l.r1 = l.r0 + l.step;
+  }
+  return l;
+}
 
 template <int D, bool F16>
-__global__ void __launch_bounds__(kJoinWarps * 32) prefix_join_kernel(const __grid_constant__ AttnParams p,
-                                                                      uint32_t* status, int ctas) {
+__global__ void __launch_bounds__(kJoinThreads) prefix_join_kernel(const __grid_constant__ AttnParams p,
+                                                                   uint32_t* status, int ctas) {
+  constexpr int kPer = D / 32;
+  __shared__ float acc_s[kJoinRows][kRowWarps][D];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (blockIdx.x == 0 && blockIdx.y == 0 && warp == 0) {
     uint32_t w = 0;
@@ -779,128 +941,127 @@ __global__ void __launch_bounds__(kJoinWarps * 32) prefix_join_kernel(const __gr
     }
     if (lane == 0) *status = w;
   }
-  // the row, and up to two items that hold parts of it
-  int it[2] = {-1, -1}, lrow[2] = {0, 0};
-  bool alt[2] = {false, false};
-  int b, kvh, rr;
+  const int slot = warp / kRowWarps, sub = warp % kRowWarps;
+  // this block's rows: of the whole call (shared mode), or of the item that CTA blockIdx.x
+  // completed
+  int item = -1;
+  Item t;
+  long long n_rows, row0 = static_cast<long long>(blockIdx.y) * kJoinRows, stride = kJoinBlocks * kJoinRows;
   if (p.shared) {
-    const long long id = static_cast<long long>(blockIdx.x) * kJoinWarps + warp;
-    if (id >= static_cast<long long>(p.Hkv) * p.B * p.R) return;
-    const int per = p.B * p.R;
-    kvh = static_cast<int>(id / per);
-    const int rg = static_cast<int>(id - static_cast<long long>(kvh) * per);
-    b = p.div_r.div(rg, &rr);
-    if (p.n_prefix > 0) {
-      const int rt = rg / kRows;
-      it[0] = kvh * p.n_rt + rt;
-      lrow[0] = rg - rt * kRows;
-      alt[0] = min(kRows, per - rt * kRows) <= 128;
-    }
-    if (p.tail_pages != nullptr) {
-      it[1] = p.n_prefix + b * p.Hkv + kvh;
-      lrow[1] = rr;
-      alt[1] = p.R <= 128;
-    }
+    n_rows = static_cast<long long>(p.Hkv) * p.B * p.R;
+    row0 = static_cast<long long>(blockIdx.x) * kJoinRows;
+    stride = static_cast<long long>(gridDim.x) * kJoinRows;
   } else {
-    const int i = p.cta_done[blockIdx.x];
-    if (i < 0) return;
-    const Item t = item_of(p, i);
-    const int r = blockIdx.y * kJoinWarps + warp;
-    if (r >= t.rows) return;
-    b = t.b;
-    kvh = t.kvh;
-    rr = t.row0 + r;
-    it[0] = i;
-    lrow[0] = r;
+    item = p.cta_done[blockIdx.x];
+    if (item < 0) return;
+    t = item_of(p, item);
+    n_rows = t.rows;
   }
-  int gh;
-  const int s = p.div_g.div(rr, &gh);
-  if (s >= queries_of(p, b)) return;
-  int first[2] = {0, 0}, n[2] = {0, 0};
-#pragma unroll
-  for (int k = 0; k < 2; ++k) {
-    if (it[k] < 0) continue;
-    const int e = it[k] - p.whole * ctas;
-    first[k] = p.first[e];
-    const int last = p.last[e];
-    if (first[k] < 0 || last < first[k] || last >= ctas) return;     // only after a wait gave up
-    n[k] = (last - first[k] + 1) * (alt[k] ? 2 : 1);
-  }
-  auto where = [&](int j) -> long long {
-    const int k = j < n[0] ? 0 : 1;
-    const int q = j - (k ? n[0] : 0);
-    const int c = first[k] + (alt[k] ? q >> 1 : q);
-    const int half = alt[k] ? (q & 1) : lrow[k] >> 7;
-    return part_row(p, it[k], c, c > first[k], half, alt[k] ? lrow[k] : lrow[k] & 127);
-  };
-  const int total = n[0] + n[1];
-  float m = -INFINITY;
-  bool nan = false;
-  for (int j = lane; j < total; j += 32) {
-    const float v = p.part_l[where(j)];
-    nan |= v != v;
-    m = fmaxf(m, v);
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-  nan = __any_sync(0xffffffffu, nan);
-  float sum = 0.f;
-  constexpr int kPer = D / 32;
-  float acc[kPer];
-#pragma unroll
-  for (int i = 0; i < kPer; ++i) acc[i] = 0.f;
-  if (m != -INFINITY) {
-#pragma unroll 4
-    for (int j = 0; j < total; ++j) {
-      const long long w = where(j);
-      const float v = p.part_l[w];
-      if (v == -INFINITY) continue;
-      const float e = exp2f(v - m);
-      sum += e;
-      const float* src = p.part_acc + w * D + lane * kPer;
-#pragma unroll
-      for (int i = 0; i < kPer; ++i) acc[i] += e * src[i];
+  for (long long base = row0; base < n_rows; base += stride) {
+    const long long id = base + slot;
+    bool live = id < n_rows;
+    int b = 0, kvh = 0, rr = 0, s = 0, gh = 0;
+    PartList l0, l1;
+    l0.n = l1.n = 0;
+    if (live) {
+      if (p.shared) {
+        const int per = p.B * p.R;
+        kvh = static_cast<int>(id / per);
+        const int rg = static_cast<int>(id - static_cast<long long>(kvh) * per);
+        b = p.div_r.div(rg, &rr);
+        if (p.n_prefix > 0) {
+          const int rt = rg / kRows;
+          l0 = parts_of(p, kvh * p.n_rt + rt, rg - rt * kRows, min(kRows, per - rt * kRows) > 128, ctas);
+        }
+        if (p.tail_pages != nullptr) l1 = parts_of(p, p.n_prefix + b * p.Hkv + kvh, rr, p.R > 128, ctas);
+      } else {
+        b = t.b;
+        kvh = t.kvh;
+        rr = t.row0 + static_cast<int>(id);
+        l0 = parts_of(p, item, static_cast<int>(id), true, ctas);
+      }
+      s = p.div_g.div(rr, &gh);
+      live = s < queries_of(p, b);
     }
-  }
-  float lse2 = m == -INFINITY ? -INFINITY : m + log2f(sum);
-  if (nan) lse2 = __int_as_float(0x7FC00000);
-  const float inv = nan ? lse2 : (sum > 0.f ? 1.f / sum : 0.f);
+    const int total = l0.n + l1.n;
+    float m = -INFINITY, sum = 0.f, acc[kPer];
+    bool nan = false;
 #pragma unroll
-  for (int i = 0; i < kPer; ++i) acc[i] *= inv;
-  const int h = kvh * p.G + gh;
-  const long long flat = (static_cast<long long>(b) * p.Hq + h) * p.Sq + s;
-  if (p.part_lse != nullptr) {
-    const float a = p.part_lse[flat] * 1.4426950408889634f;
-    if (a != -INFINITY) {
-      const float both = join(lse2, a);
-      const float wa = lse2 == -INFINITY ? 0.f : exp2f(lse2 - both), wb = exp2f(a - both);
-      const long long off = b * p.po_b + h * p.po_h + s * p.po_s + lane * kPer;
+    for (int i = 0; i < kPer; ++i) acc[i] = 0.f;
+    if (live) {
+      auto where = [&](int j) { return j < l0.n ? l0.at(j) : l1.at(j - l0.n); };
+      for (int j = lane; j < total; j += 32) {
+        const float v = p.part_l[where(j)];
+        nan |= v != v;
+        m = fmaxf(m, v);
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+      nan = __any_sync(0xffffffffu, nan);
+      if (m != -INFINITY) {
+        for (int j = lane; j < total; j += 32) sum += exp2f(p.part_l[where(j)] - m);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+#pragma unroll 4
+        for (int j = sub; j < total; j += kRowWarps) {
+          const long long w = where(j);
+          const float v = p.part_l[w];
+          const float e = exp2f(v - m);
+          const float* src = p.part_acc + w * D + lane * kPer;
+          float x[kPer];
+#pragma unroll
+          for (int i = 0; i < kPer; i += 2) *reinterpret_cast<float2*>(&x[i]) = *reinterpret_cast<const float2*>(src + i);
+          // a part without keys wrote no accumulator
+#pragma unroll
+          for (int i = 0; i < kPer; ++i) acc[i] += v == -INFINITY ? 0.f : e * x[i];
+        }
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) acc_s[slot][sub][lane * kPer + i] = acc[i];
+    __syncthreads();
+    if (live && sub == 0) {
 #pragma unroll
       for (int i = 0; i < kPer; ++i) {
-        float y;
-        if (p.part_f32) {
-          y = static_cast<const float*>(p.part_o)[off + i];
-        } else if (F16) {
-          y = __half2float(static_cast<const __half*>(p.part_o)[off + i]);
-        } else {
-          y = __bfloat162float(static_cast<const __nv_bfloat16*>(p.part_o)[off + i]);
-        }
-        acc[i] = acc[i] * wa + y * wb;
+        float x = 0.f;
+#pragma unroll
+        for (int k = 0; k < kRowWarps; ++k) x += acc_s[slot][k][lane * kPer + i];
+        acc[i] = x;
       }
-      lse2 = both;
+      float lse2 = m == -INFINITY ? -INFINITY : m + log2f(sum);
+      if (nan) lse2 = __int_as_float(0x7FC00000);
+      const float inv = nan ? lse2 : (sum > 0.f ? 1.f / sum : 0.f);
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) acc[i] *= inv;
+      const int h = kvh * p.G + gh;
+      const long long flat = (static_cast<long long>(b) * p.Hq + h) * p.Sq + s;
+      if (p.part_lse != nullptr) {
+        const float a = p.part_lse[flat] * 1.4426950408889634f;
+        if (a != -INFINITY) {
+          const float both = join(lse2, a);
+          const float wa = lse2 == -INFINITY ? 0.f : exp2f(lse2 - both), wb = exp2f(a - both);
+          const long long off = b * p.po_b + h * p.po_h + s * p.po_s + lane * kPer;
+#pragma unroll
+          for (int i = 0; i < kPer; i += 2) {
+            float2 y;
+            if (p.part_f32) y = *reinterpret_cast<const float2*>(static_cast<const float*>(p.part_o) + off + i);
+            else y = unpack2<F16>(*reinterpret_cast<const uint32_t*>(static_cast<const uint16_t*>(p.part_o) + off + i));
+            acc[i] = acc[i] * wa + y.x * wb;
+            acc[i + 1] = acc[i + 1] * wa + y.y * wb;
+          }
+          lse2 = both;
+        }
+      }
+      __syncwarp();        // every lane has read part_lse, which may be lse
+      if (p.lse != nullptr && lane == 0) p.lse[flat] = lse2 * 0.69314718055994531f;
+      const long long off = b * p.o_b + h * p.o_h + s * p.o_s + lane * kPer;
+#pragma unroll
+      for (int i = 0; i < kPer; i += 2) {
+        if (p.o_f32) *reinterpret_cast<float2*>(static_cast<float*>(p.o) + off + i) = make_float2(acc[i], acc[i + 1]);
+        else *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.o) + off + i) = pack2<F16>(acc[i], acc[i + 1]);
+      }
     }
-  }
-  __syncwarp();
-  if (p.lse != nullptr && lane == 0) p.lse[flat] = lse2 * 0.69314718055994531f;
-  const long long off = b * p.o_b + h * p.o_h + s * p.o_s + lane * kPer;
-  if (p.o_f32) {
-    float* o = static_cast<float*>(p.o) + off;
-#pragma unroll
-    for (int i = 0; i < kPer; i += 2) *reinterpret_cast<float2*>(o + i) = make_float2(acc[i], acc[i + 1]);
-  } else {
-    uint32_t* o = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.o) + off);
-#pragma unroll
-    for (int i = 0; i < kPer; i += 2) o[i / 2] = pack2<F16>(acc[i], acc[i + 1]);
+    __syncthreads();
   }
 }
 
@@ -987,12 +1148,12 @@ nabla_status launch(const AttnParams& p, const nabla_cache& cache, uint32_t* sta
   prefix_attn_kernel<D, F16><<<ctas, kThreads, C::kSmemBytes, st>>>(mk, mv, a);
   e = cudaGetLastError();
   if (e != cudaSuccess) return cuda_status(e);
-  dim3 grid(ctas, kRows / kJoinWarps);
+  dim3 grid(ctas, kJoinBlocks);
   if (a.shared) {
-    const long long rows = static_cast<long long>(a.Hkv) * a.B * a.R;
-    grid = dim3(static_cast<unsigned>((rows + kJoinWarps - 1) / kJoinWarps));
+    const long long blocks = (static_cast<long long>(a.Hkv) * a.B * a.R + kJoinRows - 1) / kJoinRows;
+    grid = dim3(static_cast<unsigned>(blocks < 1 << 20 ? blocks : 1 << 20));
   }
-  prefix_join_kernel<D, F16><<<grid, kJoinWarps * 32, 0, st>>>(a, status, ctas);
+  prefix_join_kernel<D, F16><<<grid, kJoinThreads, 0, st>>>(a, status, ctas);
   return cuda_status(cudaGetLastError());
 }
 
