@@ -13,7 +13,9 @@
 //     sequence and walks the prefix, then the sequence's tail;
 //   * shared mode (fewer rows): the rows of ALL sequences are tiled together for the
 //     prefix, so its keys and values leave HBM once for the batch; each sequence's tail is
-//     one more item, and every result is a part that the combine kernel joins.
+//     one more item, and every result is a part that the join kernel joins.
+// Items of at most 16 rows (single tokens of a group of heads) go to rows_attn_kernel, whose
+// warps stream keys on their own; all others to prefix_attn_kernel, described next.
 // The unit of scheduling is one key tile.  A CTA (one per SM) first takes whole items, one
 // per round while all CTAs have one (own mode); what is left over is cut into equal runs of
 // units, wherever they fall inside items, so no SM waits for a long item.  Item lengths
@@ -46,6 +48,8 @@ namespace {
 constexpr int kThreads = 384;
 constexpr int kSoftmaxWarp0 = 4;          // warps 4..7 = slot 0, 8..11 = slot 1
 constexpr int kMaxCtas = 148;
+constexpr int kRowCtas = 2 * kMaxCtas;    // CTAs of rows_attn_kernel
+constexpr int kFewRows = 16;              // most rows of an item of rows_attn_kernel
 constexpr int kKeys = 128;                // keys per tile
 constexpr int kRows = 256;                // query rows per item
 constexpr int kLaunchRegs = 168;
@@ -106,6 +110,7 @@ struct AttnParams {
   int n_rt;                         // row tiles: of a sequence (own), of the batch (shared)
   int n_prefix;                     // prefix items (shared mode)
   int n_items, whole;               // whole: rounds of whole items
+  int few0, few1;                   // items [few0, few1) belong to rows_attn_kernel
   int tail_half;                    // rows between the halves of a tail part
   // workspace
   uint32_t* cta_status;
@@ -114,7 +119,7 @@ struct AttnParams {
   int32_t* last;
   float* part_l;                    // log2 sums of parts
   float* part_acc;                  // normalised f32 accumulators of parts
-  long long tail_base;              // row at which the tail parts start
+  long long tail_base, few_base;    // rows at which the tail parts and the few-row parts start
 };
 
 struct Item {
@@ -177,11 +182,10 @@ __device__ __forceinline__ Item item_of(const AttnParams& p, int i) {
 __device__ __forceinline__ int length_of(const Item& t) { return max(t.np + t.nt, 1); }
 
 // A CTA's share of the work, part by part: key tiles [x0, x1) of an item.  An item counts as
-// its tiles and kSetup more (its Q, its pipeline's fill and its epilogue); a run that ends
+// its tiles and `setup` more (its Q, its pipeline's fill and its epilogue); a run that ends
 // inside an item's setup leaves the item to the next CTA.
-constexpr int kSetup = 2;
 struct Walk {
-  int round, item, x0;
+  int round, item, x0, setup;
   long long left;
   struct Part {
     int i;
@@ -201,9 +205,9 @@ struct Walk {
       o->i = item;
       o->t = item_of(p, item);
       o->total = length_of(o->t);
-      const long long end = min(static_cast<long long>(o->total + kSetup), x0 + left);
-      o->x0 = max(x0 - kSetup, 0);
-      o->x1 = max(static_cast<int>(end) - kSetup, 0);
+      const long long end = min(static_cast<long long>(o->total + setup), x0 + left);
+      o->x0 = max(x0 - setup, 0);
+      o->x1 = max(static_cast<int>(end) - setup, 0);
       left -= end - x0;
       ++item;
       x0 = 0;
@@ -214,6 +218,59 @@ struct Walk {
   }
 };
 
+// The CTA's run of units among items [i0, i1), which are cut into runs of equal length: a
+// block-wide scan of their lengths, then the thread whose items hold the run's start finds
+// it.  `scratch`: 16-byte aligned shared memory of kThreads / 32 + 8 words; all threads call it.
+constexpr int kSetup = 2, kSetupFew = 1;
+template <int kBlock>
+__device__ __forceinline__ Walk find_run(const AttnParams& p, int i0, int i1, int whole, int setup, int32_t* scratch) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  int32_t* sums = scratch + 4;
+  if (threadIdx.x == 0) scratch[0] = scratch[1] = scratch[2] = 0;
+  const int n = i1 - i0;
+  const int per = (n + kBlock - 1) / kBlock;
+  const int a = min(static_cast<int>(threadIdx.x) * per, n), b = min(a + per, n);
+  int sum = 0;
+  for (int i = a; i < b; ++i) sum += length_of(item_of(p, i0 + i)) + setup;
+  int inc = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc += v;
+  }
+  if (lane == 31) sums[warp] = inc;
+  __syncthreads();
+  int before = 0, total = 0;
+  for (int w = 0; w < kBlock / 32; ++w) {
+    if (w < warp) before += sums[w];
+    total += sums[w];
+  }
+  // every run has at least one unit, so the parts of an item are those of neighbouring CTAs
+  const int runs = min(total, static_cast<int>(gridDim.x)), run = min(static_cast<int>(blockIdx.x), runs);
+  const long long u0 = runs > 0 ? static_cast<long long>(total) * run / runs : 0;
+  const long long u1 = run < runs ? static_cast<long long>(total) * (run + 1) / runs : u0;
+  int at = before + inc - sum;                 // units before this thread's items
+  if (u1 > u0 && u0 >= at && u0 < at + sum) {
+    int i = a, len = 0;
+    for (; i < b; ++i) {
+      len = length_of(item_of(p, i0 + i)) + setup;
+      if (u0 < at + len) break;
+      at += len;
+    }
+    scratch[0] = i0 + i;
+    scratch[1] = static_cast<int>(u0 - at);
+    scratch[2] = static_cast<int>(u1 - u0);
+  }
+  __syncthreads();
+  Walk w;
+  w.round = whole > 0 ? 0 : 1 << 30;
+  w.setup = setup;
+  w.item = scratch[0];
+  w.x0 = scratch[1];
+  w.left = scratch[2];
+  return w;
+}
+
 struct Bars {
   uint64_t full[8], empty[8];       // K/V stages: landed / read
   uint64_t v_part;                  // a partial V tile landed (its tail rows are then zeroed)
@@ -222,9 +279,7 @@ struct Bars {
   uint64_t o_done[2], o_free[2];    // the part's last P V landed / the accumulator was read
   uint64_t drain;
   uint32_t tmem;
-  int32_t start_item, start_x;
-  long long start_left;
-  int32_t warp_sum[kThreads / 32 + 1];
+  alignas(16) int32_t scratch[kThreads / 32 + 8];
 };
 
 template <int D>
@@ -338,61 +393,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     mbar_init(&B.drain, 1);
     fence_mbarrier_init();
-    B.start_left = 0;
-    B.start_item = B.start_x = 0;
   }
   if (warp == 1) {
     tmem_alloc(&B.tmem, 512);
     tmem_relinquish();
   }
-  // The run of units of this CTA among the items that no round hands out whole: a block-wide
-  // scan of their lengths, then the thread whose items hold the run's start finds it.
-  {
-    const int i0 = p.whole * static_cast<int>(gridDim.x);
-    const int n = p.n_items - i0;
-    const int per = (n + kThreads - 1) / kThreads;
-    const int a = min(static_cast<int>(threadIdx.x) * per, n), b = min(a + per, n);
-    int sum = 0;
-    for (int i = a; i < b; ++i) sum += length_of(item_of(p, i0 + i)) + kSetup;
-    int inc = sum;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int v = __shfl_up_sync(0xffffffffu, inc, o);
-      if (lane >= o) inc += v;
-    }
-    if (lane == 31) B.warp_sum[warp] = inc;
-    __syncthreads();
-    int before = 0, total = 0;
-    for (int w = 0; w < kThreads / 32; ++w) {
-      if (w < warp) before += B.warp_sum[w];
-      total += B.warp_sum[w];
-    }
-    // every run has at least one unit, so the parts of an item are those of neighbouring CTAs
-    const int runs = min(total, static_cast<int>(gridDim.x)), run = min(static_cast<int>(blockIdx.x), runs);
-    const long long u0 = runs > 0 ? static_cast<long long>(total) * run / runs : 0;
-    const long long u1 = run < runs ? static_cast<long long>(total) * (run + 1) / runs : u0;
-    int at = before + inc - sum;                 // units before this thread's items
-    if (u1 > u0 && u0 >= at && u0 < at + sum) {
-      int i = a, len = 0;
-      for (; i < b; ++i) {
-        len = length_of(item_of(p, i0 + i)) + kSetup;
-        if (u0 < at + len) break;
-        at += len;
-      }
-      B.start_item = i0 + i;
-      B.start_x = static_cast<int>(u0 - at);
-      B.start_left = u1 - u0;
-    }
-  }
+  Walk walk = find_run<kThreads>(p, p.whole * static_cast<int>(gridDim.x), p.few0, p.whole, kSetup, B.scratch);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = B.tmem;
-  Walk walk;
-  walk.round = 0;
-  walk.item = B.start_item;
-  walk.x0 = B.start_x;
-  walk.left = B.start_left;
   Walk::Part part;
 
   if (warp < kSoftmaxWarp0) {
@@ -882,6 +892,287 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
+// ------------------------------------------------------------------------------------
+// Items of at most 16 rows.  Bound by the cache's bytes, and by latency when those are few:
+// a 128-row MMA tile would be mostly padding and its pipeline (8 us from launch to result)
+// longer than the work.  A CTA of four warps takes a run of units as above; a warp streams
+// every fourth group of 16 keys through its own ring in shared memory (cp.async, 24 KB in
+// flight a warp, 192 KB an SM), multiplies with m16n8k16 MMAs (the rows as M, so the
+// scores' registers are the second product's A operand), and keeps m, l and O in registers.
+// The four warps' results are joined through shared memory at the part's end.
+// ------------------------------------------------------------------------------------
+constexpr int kFewThreads = 128;
+constexpr int kFewWarps = kFewThreads / 32;
+constexpr int kGroup = 16;                 // keys of a ring stage
+
+template <int D>
+struct FewCfg {
+  static constexpr int kHalf = kGroup * D * 2;           // bytes of K (or V) of a group
+  static constexpr int kStages = D == 128 ? 3 : 6;
+  static constexpr int kWarpBytes = kStages * 2 * kHalf;
+  static constexpr int kSmemBytes = kFewWarps * kWarpBytes;
+  static_assert(kFewWarps * kFewRows * (D + 4) * 4 <= kSmemBytes, "the joined results reuse the rings");
+};
+
+__device__ __forceinline__ void ldmatrix_x4(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr));
+}
+__device__ __forceinline__ void ldmatrix_x4_trans(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr));
+}
+template <bool F16>
+__device__ __forceinline__ void mma_16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  if constexpr (F16)
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  else
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// 16 bytes, or zeros
+__device__ __forceinline__ void cp_async16_or_zero(uint32_t dst, const void* src, bool read) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(read ? 16 : 0) : "memory");
+}
+
+template <int D, bool F16>
+__global__ void __launch_bounds__(kFewThreads, 2) rows_attn_kernel(const uint16_t* __restrict__ k_pool,
+                                                                    const uint16_t* __restrict__ v_pool,
+                                                                    const __grid_constant__ AttnParams p) {
+  using C = FewCfg<D>;
+  extern __shared__ __align__(16) unsigned char smem[];
+  __shared__ __align__(16) int32_t scratch[kFewWarps + 8];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  uint32_t* status = p.cta_status + kMaxCtas + blockIdx.x;
+  if (threadIdx.x == 0) *status = 0;
+  Walk walk = find_run<kFewThreads>(p, p.few0, p.few1, 0, kSetupFew, scratch);
+  const uint32_t ring = smem_u32(smem) + warp * C::kWarpBytes;
+  constexpr float kBias = F16 ? 7.0f : 0.0f;       // as in prefix_attn_kernel
+  constexpr int kChunks = D / 8;                   // 16-byte pieces of a row
+  constexpr int kRowsPerCopy = 32 / kChunks;       // rows that one copy of the warp covers
+  const int c_row = lane / kChunks, c_ch = lane % kChunks;
+  const int q0 = lane >> 2, kq = (lane & 3) * 2;   // fragment row (and row + 8), column pair
+  Walk::Part part;
+  while (walk.next(p, &part)) {
+    const Item& t = part.t;
+    const bool pre = t.b < 0;
+    const int L = pre ? p.P : tail_of(p, t.b);
+    const int32_t* list = pre ? p.prefix_pages : p.tail_pages + static_cast<long long>(t.b) * p.tail_width;
+    const int key0 = part.x0 * kKeys;
+    const int key1 = part.n > 0 ? min(part.x1 * kKeys, L) : key0;
+    const int groups = (key1 - key0 + kGroup - 1) / kGroup;
+    const int mine = groups > warp ? (groups - warp + kFewWarps - 1) / kFewWarps : 0;
+    // page numbers of the warp's groups, 32 at a time, one per lane
+    int ids = 0;
+    auto look_up = [&](int j) {                    // groups j .. j + 31 of the warp
+      const int key = key0 + (warp + (j + lane) * kFewWarps) * kGroup;
+      ids = -1;
+      if (j + lane < mine) {
+        const int id = __ldg(list + (key >> p.page_shift));
+        if (id < 0 || id >= p.n_pages) record_status(status, kDevBadPage);
+        else ids = id;
+      }
+    };
+    auto load = [&](int j) {                       // group j of the warp into stage j % kStages
+      if ((j & 31) == 0) look_up(j);
+      const int id = __shfl_sync(0xffffffffu, ids, j & 31);
+      if (j < mine) {
+        const int key = key0 + (warp + j * kFewWarps) * kGroup;
+        const long long off = static_cast<long long>(max(id, 0)) * p.Hkv * p.page * D +
+                              (static_cast<long long>(t.kvh) * p.page + (key & (p.page - 1))) * D;
+        const uint32_t st = ring + (j % C::kStages) * 2 * C::kHalf;
+#pragma unroll
+        for (int i = 0; i < kGroup / kRowsPerCopy; ++i) {
+          const int r = i * kRowsPerCopy + c_row;
+          const uint32_t dst = st + r * D * 2 + ((c_ch ^ (r & 7)) << 4);
+          // a bad page, and slots past the length, are read as zeros
+          const bool read = id >= 0 && key + r < key1;
+          const long long src = off + (read ? r * D + c_ch * 8 : 0);
+          cp_async16_or_zero(dst, k_pool + src, read);
+          cp_async16_or_zero(dst + C::kHalf, v_pool + src, read);
+        }
+      }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+#pragma unroll
+    for (int j = 0; j < C::kStages - 1; ++j) load(j);
+
+    // The thread's two rows: keys they see, and their Q in A-operand registers.
+    int lim[2];
+    uint32_t qf[D / 16][4];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int r = q0 + 8 * e;
+      const uint16_t* src = nullptr;
+      lim[e] = 0;
+      if (r < t.rows) {
+        int b = t.b, rr = t.row0 + r, g;
+        if (b < 0) b = p.div_r.div(rr, &rr);
+        const int s = p.div_g.div(rr, &g);
+        const int n = queries_of(p, b);
+        if (s < n) {
+          const int v = visible(p, tail_of(p, b), n, s);
+          lim[e] = pre ? min(v, p.P) : v - p.P;
+          src = static_cast<const uint16_t*>(p.q) + b * p.q_b + (t.kvh * p.G + g) * p.q_h + s * p.q_s + kq;
+        }
+      }
+#pragma unroll
+      for (int c = 0; c < D / 16; ++c) {
+        qf[c][e] = src != nullptr ? *reinterpret_cast<const uint32_t*>(src + c * 16) : 0u;
+        qf[c][2 + e] = src != nullptr ? *reinterpret_cast<const uint32_t*>(src + c * 16 + 8) : 0u;
+      }
+    }
+    float o[D / 8][4];
+#pragma unroll
+    for (int c = 0; c < D / 8; ++c)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) o[c][i] = 0.f;
+    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+    for (int j = 0; j < mine; ++j) {
+      asm volatile("cp.async.wait_group %0;" ::"n"(C::kStages - 2) : "memory");
+      __syncwarp();                                // every lane's copies of group j; stage j - 1 is read
+      load(j + C::kStages - 1);
+      const uint32_t st = ring + (j % C::kStages) * 2 * C::kHalf;
+      const int key = key0 + (warp + j * kFewWarps) * kGroup;
+      float sc[2][4];
+#pragma unroll
+      for (int n = 0; n < 2; ++n)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) sc[n][i] = 0.f;
+#pragma unroll
+      for (int n = 0; n < 2; ++n) {
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) {         // 32 channels: four 8 x 8 matrices
+          const int r = n * 8 + (lane & 7), ch = c * 4 + (lane >> 3);
+          uint32_t kf[4];
+          ldmatrix_x4(kf, st + r * D * 2 + ((ch ^ (r & 7)) << 4));
+          mma_16816<F16>(sc[n], qf[2 * c], kf[0], kf[1]);
+          mma_16816<F16>(sc[n], qf[2 * c + 1], kf[2], kf[3]);
+        }
+      }
+      float mx[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+      for (int n = 0; n < 2; ++n)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int e = i >> 1;
+          if (key + n * 8 + kq + (i & 1) >= lim[e]) sc[n][i] = -INFINITY;
+          mx[e] = fmaxf(mx[e], sc[n][i]);
+        }
+      float factor[2] = {1.f, 1.f};
+      bool rescale = false;
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], 1));
+        mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], 2));
+        const float rm = mx[e] * p.scale_log2 - kBias;
+        if (mx[e] != -INFINITY && rm > m[e] + 8.0f) {
+          if (m[e] != -INFINITY) {
+            factor[e] = fast_exp2(m[e] - rm);
+            rescale = true;
+          }
+          m[e] = rm;
+        }
+      }
+      if (__any_sync(0xffffffffu, rescale)) {
+#pragma unroll
+        for (int c = 0; c < D / 8; ++c)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) o[c][i] *= factor[i >> 1];
+        l[0] *= factor[0];
+        l[1] *= factor[1];
+      }
+      uint32_t pf[4];
+#pragma unroll
+      for (int n = 0; n < 2; ++n)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const float neg = m[e] == -INFINITY ? 0.f : -m[e];
+          const float x = fast_exp2(fmaf(sc[n][2 * e], p.scale_log2, neg));
+          const float y = fast_exp2(fmaf(sc[n][2 * e + 1], p.scale_log2, neg));
+          l[e] += x + y;
+          pf[2 * n + e] = pack2<F16>(x, y);
+        }
+#pragma unroll
+      for (int c = 0; c < D / 16; ++c) {           // 16 channels: two tiles of 8, two halves of the keys
+        const int r = (lane & 7) + (lane & 8), ch = c * 2 + (lane >> 4);
+        uint32_t vf[4];
+        ldmatrix_x4_trans(vf, st + C::kHalf + r * D * 2 + ((ch ^ (r & 7)) << 4));
+        mma_16816<F16>(o[2 * c], pf, vf[0], vf[1]);
+        mma_16816<F16>(o[2 * c + 1], pf, vf[2], vf[3]);
+      }
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      l[e] += __shfl_xor_sync(0xffffffffu, l[e], 1);
+      l[e] += __shfl_xor_sync(0xffffffffu, l[e], 2);
+    }
+    // Join the warps (the rings are free now): rows of D values, then m and l.
+    __syncthreads();
+    constexpr int kPitch = D + 4;
+    float* acc = reinterpret_cast<float*>(smem);
+    __shared__ float stat[kFewWarps][kFewRows][2];
+#pragma unroll
+    for (int c = 0; c < D / 8; ++c) {
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+        *reinterpret_cast<float2*>(acc + (warp * kFewRows + q0 + 8 * e) * kPitch + c * 8 + kq) =
+            make_float2(o[c][2 * e], o[c][2 * e + 1]);
+    }
+    if ((lane & 3) == 0) {
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        stat[warp][q0 + 8 * e][0] = m[e];
+        stat[warp][q0 + 8 * e][1] = l[e];
+      }
+    }
+    __syncthreads();
+    if (threadIdx.x == 0) {
+      if (part.x0 == 0) p.first[part.i] = blockIdx.x;
+      if (part.x1 == part.total) p.last[part.i] = blockIdx.x;
+    }
+    constexpr int kPerRow = kFewThreads / kFewRows;                 // 8 threads a row
+    const int r = threadIdx.x / kPerRow;
+    if (r < t.rows) {
+      int b = t.b, rr = t.row0 + r, g;
+      if (b < 0) b = p.div_r.div(rr, &rr);
+      const int s = p.div_g.div(rr, &g);
+      if (s < queries_of(p, b)) {
+        float top = -INFINITY, sum = 0.f, w[kFewWarps];
+#pragma unroll
+        for (int k = 0; k < kFewWarps; ++k) top = fmaxf(top, stat[k][r][0]);
+#pragma unroll
+        for (int k = 0; k < kFewWarps; ++k) {
+          const float lk = stat[k][r][1];
+          w[k] = lk == 0.f ? 0.f : exp2f(stat[k][r][0] - top);
+          sum += lk == 0.f ? 0.f : w[k] * lk;
+        }
+        const long long row = p.few_base + static_cast<long long>(part.i - p.few0 + blockIdx.x) * kFewRows + r;
+        const float inv = sum == 0.f ? 0.f : 1.f / sum;
+        if (threadIdx.x % kPerRow == 0) p.part_l[row] = sum == 0.f ? -INFINITY : top + log2f(sum);
+#pragma unroll
+        for (int i = 0; i < D / (4 * kPerRow); ++i) {
+          const int d = 4 * (threadIdx.x % kPerRow + i * kPerRow);
+          float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+          for (int k = 0; k < kFewWarps; ++k) {
+            const float4 x = *reinterpret_cast<const float4*>(acc + (k * kFewRows + r) * kPitch + d);
+            f.x += w[k] * x.x; f.y += w[k] * x.y; f.z += w[k] * x.z; f.w += w[k] * x.w;
+          }
+          *reinterpret_cast<float4*>(p.part_acc + row * D + d) = make_float4(f.x * inv, f.y * inv, f.z * inv, f.w * inv);
+        }
+      }
+    }
+    __syncthreads();
+  }
+}
+
 // Joins the parts of split items, merges the caller's part and writes the rows; block 0
 // also gathers the CTAs' status words and looks the lengths over.  Four warps share a row: a
 // long prefix leaves a row up to two parts per CTA, which are read in parallel (every fourth
@@ -905,7 +1196,15 @@ __device__ __forceinline__ PartList parts_of(const AttnParams& p, int i, int lro
   const int e = i - p.whole * ctas;
   const int first = p.first[e], last = p.last[e];
   l.n = 0;
-  if (first < 0 || last < first || last >= ctas) return l;       // only after a wait gave up
+  const bool few = i >= p.few0 && i < p.few1;
+  if (first < 0 || last < first || last >= (few ? kRowCtas : ctas)) return l;       // only after a wait gave up
+  if (few) {
+    l.n = last - first + 1;
+    l.step = kFewRows;
+    l.r0 = p.few_base + static_cast<long long>(i - p.few0 + first) * kFewRows + lrow;
+    l.r1 = l.r0 + l.step;
+    return l;
+  }
   const int half = dual ? lrow >> 7 : 0, row = dual ? lrow & 127 : lrow;
   l.r0 = part_row(p, i, first, false, half, row);
   if (!p.shared) {
@@ -922,14 +1221,17 @@ __device__ __forceinline__ PartList parts_of(const AttnParams& p, int i, int lro
 
 template <int D, bool F16>
 __global__ void __launch_bounds__(kJoinThreads) prefix_join_kernel(const __grid_constant__ AttnParams p,
-                                                                   uint32_t* status, int ctas) {
+                                                                   uint32_t* status, int ctas, int few_ctas) {
   constexpr int kPer = D / 32;
   __shared__ float acc_s[kJoinRows][kRowWarps][D];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (blockIdx.x == 0 && blockIdx.y == 0 && warp == 0) {
     uint32_t w = 0;
-    for (int c = lane; c < ctas; c += 32)
-      if (w == 0) w = p.cta_status[c];
+    for (int c = lane; c < kMaxCtas + kRowCtas; c += 32) {
+      // the words of the kernels that ran
+      const bool ran = c < kMaxCtas ? p.few0 > 0 && c < ctas : p.few1 > p.few0 && c < kMaxCtas + few_ctas;
+      if (ran && w == 0) w = p.cta_status[c];
+    }
     for (int i = lane; i < p.B; i += 32) {
       if (p.q_len != nullptr && queries_of(p, i) != p.q_len[i] && w == 0) w = kDevBadLength;
       if (p.tail_pages != nullptr && tail_of(p, i) != p.tail_len[i] && w == 0) w = kDevBadLength;
@@ -1086,7 +1388,8 @@ bool make_map_pool(CUtensorMap* map, const void* base, const nabla_cache& c) {
 struct Plan {
   bool shared;
   long long n_rt, n_prefix, n_tail, n_items;
-  long long prefix_rows, tail_rows;      // rows of parts
+  bool few_prefix, few_tail;             // items of rows_attn_kernel
+  long long prefix_rows, tail_rows, few_rows;      // rows of parts
   size_t off_first, off_last, off_l, off_acc, bytes;
 };
 
@@ -1099,9 +1402,14 @@ Plan make_plan(long long B, long long Hkv, long long G, long long Sq, int D) {
     a.n_prefix = Hkv * a.n_rt;
     a.n_tail = B * Hkv;
     a.n_items = a.n_prefix + a.n_tail;
-    a.prefix_rows = (a.n_prefix + kMaxCtas) * kRows;
-    a.tail_rows = (a.n_tail + kMaxCtas) * 2 * (R < 128 ? R : 128);
+    a.few_prefix = B * R <= kFewRows;
+    a.few_tail = R <= kFewRows;
+    a.prefix_rows = a.few_prefix ? 0 : (a.n_prefix + kMaxCtas) * kRows;
+    a.tail_rows = a.few_tail ? 0 : (a.n_tail + kMaxCtas) * 2 * (R < 128 ? R : 128);
+    a.few_rows = a.few_tail ? (a.n_items + kRowCtas) * kFewRows : 0;
   } else {
+    a.few_prefix = a.few_tail = false;
+    a.few_rows = 0;
     a.n_rt = (R + kRows - 1) / kRows;
     a.n_prefix = a.n_tail = 0;
     a.n_items = B * Hkv * a.n_rt;
@@ -1109,11 +1417,12 @@ Plan make_plan(long long B, long long Hkv, long long G, long long Sq, int D) {
     a.tail_rows = 0;
   }
   const long long split = a.shared ? a.n_items : kMaxCtas;
-  a.off_first = kStatusBytes + 2 * 1024;
+  a.off_first = kStatusBytes + 2048 + 1024;
   a.off_last = a.off_first + align_up(split * 4, 256);
   a.off_l = a.off_last + align_up(split * 4, 256);
-  a.off_acc = a.off_l + align_up((a.prefix_rows + a.tail_rows) * 4, 256);
-  a.bytes = a.off_acc + static_cast<size_t>(a.prefix_rows + a.tail_rows) * D * 4;
+  const long long rows = a.prefix_rows + a.tail_rows + a.few_rows;
+  a.off_acc = a.off_l + align_up(rows * 4, 256);
+  a.bytes = a.off_acc + static_cast<size_t>(rows) * D * 4;
   return a;
 }
 
@@ -1129,31 +1438,44 @@ nabla_status check_sizes(int64_t B, int64_t Hq, int64_t Hkv, int64_t Sq, int D) 
 template <int D, bool F16>
 nabla_status launch(const AttnParams& p, const nabla_cache& cache, uint32_t* status, cudaStream_t st) {
   using C = Cfg<D>;
-  CUtensorMap mk, mv;
-  if (!make_map_pool(&mk, cache.k, cache) || !make_map_pool(&mv, cache.v, cache)) return NABLA_ERR_CUDA;
-  cudaError_t e = cudaFuncSetAttribute(prefix_attn_kernel<D, F16>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
-  if (e != cudaSuccess) return cuda_status(e);
-  // The register split needs the block to launch with kLaunchRegs a thread.
-  cudaFuncAttributes fa;
-  e = cudaFuncGetAttributes(&fa, prefix_attn_kernel<D, F16>);
-  if (e != cudaSuccess) return cuda_status(e);
-  if (fa.numRegs != kLaunchRegs) return NABLA_ERR_UNSUPPORTED;
   int dev = 0, sms = kMaxCtas;
-  e = cudaGetDevice(&dev);
+  cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return cuda_status(e);
-  const int ctas = sms < kMaxCtas ? sms : kMaxCtas;
+  const int ctas = sms < kMaxCtas ? sms : kMaxCtas, few_ctas = 2 * ctas;
   AttnParams a = p;
   a.whole = a.shared ? 0 : a.n_items / ctas;
-  prefix_attn_kernel<D, F16><<<ctas, kThreads, C::kSmemBytes, st>>>(mk, mv, a);
-  e = cudaGetLastError();
-  if (e != cudaSuccess) return cuda_status(e);
+  CUtensorMap mk, mv;
+  if (a.few0 > 0) {
+    if (!make_map_pool(&mk, cache.k, cache) || !make_map_pool(&mv, cache.v, cache)) return NABLA_ERR_CUDA;
+    e = cudaFuncSetAttribute(prefix_attn_kernel<D, F16>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
+    if (e != cudaSuccess) return cuda_status(e);
+    // The register split needs the block to launch with kLaunchRegs a thread.
+    cudaFuncAttributes fa;
+    e = cudaFuncGetAttributes(&fa, prefix_attn_kernel<D, F16>);
+    if (e != cudaSuccess) return cuda_status(e);
+    if (fa.numRegs != kLaunchRegs) return NABLA_ERR_UNSUPPORTED;
+  }
+  if (a.few1 > a.few0) {
+    using F = FewCfg<D>;
+    e = cudaFuncSetAttribute(rows_attn_kernel<D, F16>, cudaFuncAttributeMaxDynamicSharedMemorySize, F::kSmemBytes);
+    if (e != cudaSuccess) return cuda_status(e);
+    rows_attn_kernel<D, F16><<<few_ctas, kFewThreads, F::kSmemBytes, st>>>(
+        static_cast<const uint16_t*>(cache.k), static_cast<const uint16_t*>(cache.v), a);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return cuda_status(e);
+  }
+  if (a.few0 > 0) {
+    prefix_attn_kernel<D, F16><<<ctas, kThreads, C::kSmemBytes, st>>>(mk, mv, a);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return cuda_status(e);
+  }
   dim3 grid(ctas, kJoinBlocks);
   if (a.shared) {
     const long long blocks = (static_cast<long long>(a.Hkv) * a.B * a.R + kJoinRows - 1) / kJoinRows;
     grid = dim3(static_cast<unsigned>(blocks < 1 << 20 ? blocks : 1 << 20));
   }
-  prefix_join_kernel<D, F16><<<grid, kJoinThreads, 0, st>>>(a, status, ctas);
+  prefix_join_kernel<D, F16><<<grid, kJoinThreads, 0, st>>>(a, status, ctas, few_ctas);
   return cuda_status(cudaGetLastError());
 }
 
@@ -1261,14 +1583,17 @@ extern "C" nabla_status nabla_prefix_attn(nabla_heads q, int32_t B, int32_t Sq, 
   p.n_prefix = plan.shared && (prefix_len > 0 || !tail_pages) ? static_cast<int>(plan.n_prefix) : 0;
   p.n_items = plan.shared ? p.n_prefix + (tail_pages ? static_cast<int>(plan.n_tail) : 0) : static_cast<int>(plan.n_items);
   p.tail_half = p.R < 128 ? p.R : 128;
+  p.few0 = !plan.few_tail ? p.n_items : (plan.few_prefix ? 0 : p.n_prefix);
+  p.few1 = p.n_items;
   char* ws = static_cast<char*>(workspace);
   p.cta_status = reinterpret_cast<uint32_t*>(ws + kStatusBytes);
-  p.cta_done = reinterpret_cast<int32_t*>(ws + kStatusBytes + 1024);
+  p.cta_done = reinterpret_cast<int32_t*>(ws + kStatusBytes + 2048);
   p.first = reinterpret_cast<int32_t*>(ws + plan.off_first);
   p.last = reinterpret_cast<int32_t*>(ws + plan.off_last);
   p.part_l = reinterpret_cast<float*>(ws + plan.off_l);
   p.part_acc = reinterpret_cast<float*>(ws + plan.off_acc);
   p.tail_base = plan.prefix_rows;
+  p.few_base = plan.prefix_rows + plan.tail_rows;
   uint32_t* status = static_cast<uint32_t*>(workspace);
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   if (cache.D == 64)
