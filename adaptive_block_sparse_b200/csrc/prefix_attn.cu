@@ -111,7 +111,7 @@ struct AttnParams {
   int n_prefix;                     // prefix items (shared mode)
   int n_items, whole;               // whole: rounds of whole items
   int few0, few1;                   // items [few0, few1) belong to rows_attn_kernel
-  int tail_half;                    // rows between the halves of a tail part
+  int tail_rows;                    // rows of a tail part
   // workspace
   uint32_t* cta_status;
   int32_t* cta_done;                // own mode: the split item that CTA c completes, or -1
@@ -318,11 +318,18 @@ __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 
+// Barrier of two warps (ids 1 ..; 0 is __syncthreads).
+__device__ __forceinline__ void pair_sync(int id) { asm volatile("barrier.cta.sync %0, 64;" ::"r"(id) : "memory"); }
+
+// The next kernel of the call may be set up from here on / waits here for the ones before.
+__device__ __forceinline__ void next_kernel_may_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_for_kernel_before() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 // Rows of a part in the workspace (row-major: rows of D floats, and one log-sum each).
 __device__ __forceinline__ long long part_row(const AttnParams& p, int i, int cta, bool cont, int half, int row) {
   if (!p.shared) return (static_cast<long long>(2 * cta + (cont ? 0 : 1)) * 2 + half) * 128 + row;
   if (i < p.n_prefix) return (static_cast<long long>(i + cta) * 2 + half) * 128 + row;
-  return p.tail_base + (static_cast<long long>(i - p.n_prefix + cta) * 2 + half) * p.tail_half + row;
+  return p.tail_base + static_cast<long long>(i - p.n_prefix + cta) * p.tail_rows + half * 128 + row;
 }
 
 // 2^y for a pair of arguments, without the special-function unit: y = n + f with n
@@ -375,6 +382,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   uint32_t* status = p.cta_status + blockIdx.x;
 
+  next_kernel_may_start();
   if (threadIdx.x == 0) {
     *status = 0;
     p.cta_done[blockIdx.x] = -1;
@@ -582,12 +590,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
     } else {
       // ------------------------------------------------------------------ Q rows
-      // 64 threads gather the tile's rows into the K-major 128-byte-swizzled layout, a row by
-      // D / 8 neighbouring threads; rows that do not exist are zeros.
+      // Two warps gather the tile's rows into the K-major 128-byte-swizzled layout, each every
+      // other 32 rows: a lane finds one row, then the warp copies the rows, D / 8 lanes a row.
+      // Rows that do not exist are zeros.
       constexpr int kChunks = D / 8;
-      const int tid = threadIdx.x - 64;
-      const int c = tid % kChunks, r_first = tid / kChunks;
-      constexpr int kStep = 64 / kChunks;
+      constexpr int kStep = 32 / kChunks;
+      const int c = lane % kChunks;
       const uint16_t* q = static_cast<const uint16_t*>(p.q);
       uint32_t n_q = 0;
       bool ok = true;
@@ -597,17 +605,22 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (n_q > 0) ok = __all_sync(0xffffffffu, bar_wait(&B.q_empty, (n_q - 1) & 1, status, kDevTimeoutQFull));
         if (!ok) break;
         ++n_q;
-#pragma unroll 4
-        for (int r = r_first; r < n_rows; r += kStep) {
-          unsigned char* dst = smem + (r >> 7) * C::kTileBytes + (c >> 3) * 16384 + (r & 127) * 128 +
-                               (((c & 7) ^ (r & 7)) << 4);
-          if (r < part.t.rows) {
-            int b = part.t.b, rr = part.t.row0 + r, g;
+        for (int r0 = (warp - 2) * 32; r0 < n_rows; r0 += 64) {
+          long long off = -1;
+          if (r0 + lane < part.t.rows) {
+            int b = part.t.b, rr = part.t.row0 + r0 + lane, g;
             if (b < 0) b = p.div_r.div(rr, &rr);
             const int s = p.div_g.div(rr, &g);
-            cp_async16(smem_u32(dst), q + b * p.q_b + (part.t.kvh * p.G + g) * p.q_h + s * p.q_s + c * 8);
-          } else {
-            *reinterpret_cast<uint4*>(dst) = make_uint4(0u, 0u, 0u, 0u);
+            off = b * p.q_b + (part.t.kvh * p.G + g) * p.q_h + s * p.q_s;
+          }
+#pragma unroll 4
+          for (int i = 0; i < 32; i += kStep) {
+            const int r = r0 + i + lane / kChunks;
+            const long long from = __shfl_sync(0xffffffffu, off, r & 31);
+            unsigned char* dst = smem + (r >> 7) * C::kTileBytes + (c >> 3) * 16384 + (r & 127) * 128 +
+                                 (((c & 7) ^ (r & 7)) << 4);
+            if (from >= 0) cp_async16(smem_u32(dst), q + from + c * 8);
+            else *reinterpret_cast<uint4*>(dst) = make_uint4(0u, 0u, 0u, 0u);
           }
         }
         asm volatile("cp.async.wait_all;" ::: "memory");
@@ -631,8 +644,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     // long prefix has enough small ones to matter).
     constexpr float kBias = F16 ? 7.0f : 0.0f;
     uint32_t n_s = 0, n_o = 0;
-    bool ok = true;
-    while (ok && walk.next(p, &part)) {
+    const int pair = 1 + (warp & 3);     // barrier of the two slots' warps of the same TMEM lanes
+    unsigned char* stage = smem + C::kOffOut + (warp - kSoftmaxWarp0) * 4096;
+    // A wait that gives up (never, short of a fault) only ends the waiting: the slots' warps go
+    // on through the same barriers, so neither is left at one.
+    bool dead = false;
+    auto wait = [&](uint64_t* bar, uint32_t parity, uint32_t code) {
+      if (!dead) dead = !__all_sync(0xffffffffu, bar_wait(bar, parity, status, code));
+    };
+    while (walk.next(p, &part)) {
       // the row: its sequence, query and head, and the keys it sees
       const int r = part.t.dual ? slot * 128 + row : row;
       int b = part.t.b, s = 0, gh = 0;
@@ -657,8 +677,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool any = false;
       for (int x = x_first; x < xe; x += stride) {
         any = true;
-        ok = __all_sync(0xffffffffu, bar_wait(&B.s_full[slot], n_s & 1, status, kDevTimeoutSFull));
-        if (!ok) break;
+        wait(&B.s_full[slot], n_s & 1, kDevTimeoutSFull);
         tc_fence_after();
         const int seen = x < part.t.np ? lim_p - x * kKeys : lim_t - (x - part.t.np) * kKeys;
         float2 acc = make_float2(0.f, 0.f);
@@ -759,17 +778,38 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) mbar_arrive(&B.p_full[slot]);
         ++n_s;
       }
-      if (!ok) break;
       // ------------------------------------------------------------------ the part's result
       if (any) {
-        ok = __all_sync(0xffffffffu, bar_wait(&B.o_done[slot], n_o & 1, status, kDevTimeoutOBar));
-        if (!ok) break;
+        wait(&B.o_done[slot], n_o & 1, kDevTimeoutOBar);
         ++n_o;
         tc_fence_after();
       }
       // l is NaN where a visible score is: such a row is NaN, not empty
       float inv = l == 0.f ? 0.f : 1.f / l;
       float sum2 = l == 0.f ? -INFINITY : m_ref + log2f(l);
+      // With the same rows in both slots, their results are joined here: each slot's warps
+      // read both accumulators and write half of the channels.
+      const bool dual = part.t.dual;
+      float inv_other = 0.f;
+      const bool any_other = !dual && part.n > 1 - slot;
+      if (!dual) {
+        volatile float* mine = reinterpret_cast<volatile float*>(stage + lane * 8);
+        mine[0] = m_ref;
+        mine[1] = l;
+        tc_fence_before();
+        pair_sync(pair);
+        tc_fence_after();
+        const volatile float* x = reinterpret_cast<const volatile float*>(
+            smem + C::kOffOut + ((warp - kSoftmaxWarp0) ^ 4) * 4096 + lane * 8);
+        const float m_o = x[0], l_o = x[1];
+        pair_sync(pair);                 // the staging areas may be overwritten
+        const float top = fmaxf(m_ref, m_o);
+        const float wa = l == 0.f ? 0.f : exp2f(m_ref - top), wb = l_o == 0.f ? 0.f : exp2f(m_o - top);
+        const float sum = (l == 0.f ? 0.f : wa * l) + (l_o == 0.f ? 0.f : wb * l_o);
+        sum2 = sum == 0.f ? -INFINITY : top + log2f(sum);
+        inv = sum == 0.f ? 0.f : wa / sum;
+        inv_other = sum == 0.f ? 0.f : wb / sum;
+      }
       const bool whole = !p.shared && part.x0 == 0 && part.x1 == part.total;
       // where the row goes: bit 0 of `how` = written, bit 1 = merged with the caller's part
       long long at = 0, part_at = 0;
@@ -801,8 +841,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!p.shared && part.x0 > 0) p.cta_done[blockIdx.x] = part.i;
         }
         if (valid) {
-          const long long w = part_row(p, part.i, blockIdx.x, part.x0 > 0, slot, row);
-          p.part_l[w] = sum2;
+          const long long w = part_row(p, part.i, blockIdx.x, part.x0 > 0, dual ? slot : 0, row);
+          if (dual || slot == 0) p.part_l[w] = sum2;
           how = sum2 != -INFINITY ? 1 : 0;
           at = w * D;
         }
@@ -811,7 +851,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       // covers whole 128-byte lines (8 lanes a row) instead of 16 bytes of 32 rows: 5 us
       // less per item of 128 f32 rows.
       const bool to_f32 = !whole || p.o_f32;
-      unsigned char* stage = smem + C::kOffOut + (warp - kSoftmaxWarp0) * 4096;
       // the rows whose channels 4 ch .. 4 ch + 3 (of every 32) this lane stores
       const int ch = lane & 7;
       long long to[8];
@@ -823,22 +862,33 @@ __global__ void __launch_bounds__(kThreads, 1)
         hows |= static_cast<uint32_t>(__shfl_sync(0xffffffffu, how, rr)) << (2 * it);
       }
       const bool merge = __any_sync(0xffffffffu, (how & 2) != 0);
+      const int d_end = dual ? D : (slot + 1) * (D / 2);
+#pragma unroll 1
+      for (int d0 = dual ? 0 : slot * (D / 2); d0 < d_end; d0 += 32) {
+        float a[32];
 #pragma unroll
-      for (int d0 = 0; d0 < D; d0 += 32) {
-        uint32_t a[32];
+        for (int i = 0; i < 32; ++i) a[i] = 0.f;
         if (any) {
-          tmem_ld32(o_col + d0, a);
+          uint32_t x[32];
+          tmem_ld32(o_col + d0, x);
           tmem_wait_ld();
-          reg_fence32(a);
-        }
-        if (any && d0 + 32 == D) {
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&B.o_free[slot]);
-        }
-        if (!any || inv == 0.f) {
+          reg_fence32(x);
 #pragma unroll
-          for (int i = 0; i < 32; ++i) a[i] = 0u;
+          for (int i = 0; i < 32; ++i) a[i] = inv == 0.f ? 0.f : __uint_as_float(x[i]) * inv;
+        }
+        if (any_other) {
+          uint32_t x[32];
+          tmem_ld32(tmem + lane_base + C::col_o(slot ^ 1) + d0, x);
+          tmem_wait_ld();
+          reg_fence32(x);
+#pragma unroll
+          for (int i = 0; i < 32; ++i) a[i] += inv_other == 0.f ? 0.f : __uint_as_float(x[i]) * inv_other;
+        }
+        if (d0 + 32 == d_end) {
+          tc_fence_before();
+          if (!dual) pair_sync(pair);      // the other slot's warp has read it too
+          __syncwarp();
+          if (any && lane == 0) mbar_arrive(&B.o_free[slot]);
         }
         float4 y[8];
         if (merge) {
@@ -861,8 +911,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int i = 0; i < 8; ++i)
           *reinterpret_cast<float4*>(stage + lane * 128 + ((i ^ (lane & 7)) << 4)) =
-              make_float4(__uint_as_float(a[4 * i]) * inv, __uint_as_float(a[4 * i + 1]) * inv,
-                          __uint_as_float(a[4 * i + 2]) * inv, __uint_as_float(a[4 * i + 3]) * inv);
+              make_float4(a[4 * i], a[4 * i + 1], a[4 * i + 2], a[4 * i + 3]);
         __syncwarp();
 #pragma unroll
         for (int it = 0; it < 8; ++it) {
@@ -890,6 +939,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
+  // The join kernel waits for this one only: end after rows_attn_kernel.
+  if (threadIdx.x == 0) wait_for_kernel_before();
 }
 
 // ------------------------------------------------------------------------------------
@@ -949,6 +1000,7 @@ __global__ void __launch_bounds__(kFewThreads, 2) rows_attn_kernel(const uint16_
   __shared__ __align__(16) int32_t scratch[kFewWarps + 8];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   uint32_t* status = p.cta_status + kMaxCtas + blockIdx.x;
+  next_kernel_may_start();
   if (threadIdx.x == 0) *status = 0;
   Walk walk = find_run<kFewThreads>(p, p.few0, p.few1, 0, kSetupFew, scratch);
   const uint32_t ring = smem_u32(smem) + warp * C::kWarpBytes;
@@ -1191,7 +1243,7 @@ struct PartList {
   __device__ __forceinline__ long long at(int j) const { return j == 0 ? r0 : r1 + static_cast<long long>(j - 1) * step; }
 };
 
-__device__ __forceinline__ PartList parts_of(const AttnParams& p, int i, int lrow, bool dual, int ctas) {
+__device__ __forceinline__ PartList parts_of(const AttnParams& p, int i, int lrow, int ctas) {
   PartList l;
   const int e = i - p.whole * ctas;
   const int first = p.first[e], last = p.last[e];
@@ -1205,15 +1257,15 @@ __device__ __forceinline__ PartList parts_of(const AttnParams& p, int i, int lro
     l.r1 = l.r0 + l.step;
     return l;
   }
-  const int half = dual ? lrow >> 7 : 0, row = dual ? lrow & 127 : lrow;
+  const int half = lrow >> 7, row = lrow & 127;
   l.r0 = part_row(p, i, first, false, half, row);
   if (!p.shared) {
     l.n = last - first + 1;
     l.r1 = part_row(p, i, first + 1, true, half, row);
     l.step = 4 * 128;
   } else {
-    l.n = (last - first + 1) * (dual ? 1 : 2);
-    l.step = (i < p.n_prefix ? 128 : p.tail_half) * (dual ? 2 : 1);
+    l.n = last - first + 1;
+    l.step = i < p.n_prefix ? kRows : p.tail_rows;
     l.r1 = l.r0 + l.step;
   }
   return l;
@@ -1225,6 +1277,7 @@ __global__ void __launch_bounds__(kJoinThreads) prefix_join_kernel(const __grid_
   constexpr int kPer = D / 32;
   __shared__ float acc_s[kJoinRows][kRowWarps][D];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  wait_for_kernel_before();
   if (blockIdx.x == 0 && blockIdx.y == 0 && warp == 0) {
     uint32_t w = 0;
     for (int c = lane; c < kMaxCtas + kRowCtas; c += 32) {
@@ -1273,14 +1326,14 @@ __global__ void __launch_bounds__(kJoinThreads) prefix_join_kernel(const __grid_
         b = p.div_r.div(rg, &rr);
         if (p.n_prefix > 0) {
           const int rt = rg / kRows;
-          l0 = parts_of(p, kvh * p.n_rt + rt, rg - rt * kRows, min(kRows, per - rt * kRows) > 128, ctas);
+          l0 = parts_of(p, kvh * p.n_rt + rt, rg - rt * kRows, ctas);
         }
-        if (p.tail_pages != nullptr) l1 = parts_of(p, p.n_prefix + b * p.Hkv + kvh, rr, p.R > 128, ctas);
+        if (p.tail_pages != nullptr) l1 = parts_of(p, p.n_prefix + b * p.Hkv + kvh, rr, ctas);
       } else {
         b = t.b;
         kvh = t.kvh;
         rr = t.row0 + static_cast<int>(id);
-        l0 = parts_of(p, item, static_cast<int>(id), true, ctas);
+        l0 = parts_of(p, item, static_cast<int>(id), ctas);
       }
       s = p.div_g.div(rr, &gh);
       live = s < queries_of(p, b);
@@ -1405,7 +1458,7 @@ Plan make_plan(long long B, long long Hkv, long long G, long long Sq, int D) {
     a.few_prefix = B * R <= kFewRows;
     a.few_tail = R <= kFewRows;
     a.prefix_rows = a.few_prefix ? 0 : (a.n_prefix + kMaxCtas) * kRows;
-    a.tail_rows = a.few_tail ? 0 : (a.n_tail + kMaxCtas) * 2 * (R < 128 ? R : 128);
+    a.tail_rows = a.few_tail ? 0 : (a.n_tail + kMaxCtas) * (R <= 128 ? R : kRows);
     a.few_rows = a.few_tail ? (a.n_items + kRowCtas) * kFewRows : 0;
   } else {
     a.few_prefix = a.few_tail = false;
@@ -1433,6 +1486,24 @@ nabla_status check_sizes(int64_t B, int64_t Hq, int64_t Hkv, int64_t Sq, int D) 
   const double rows = static_cast<double>(B) * (Hq / Hkv) * Sq;
   if (rows >= 1073741824.0 || static_cast<double>(B) * Hkv + rows / 256 * Hkv >= 1048576.0 * 8) return NABLA_ERR_UNSUPPORTED;
   return NABLA_OK;
+}
+
+// A launch that may be set up while the kernel before it in the stream still runs (that
+// kernel lets it, and the kernel itself waits where it must).
+template <typename... Params, typename... Args>
+cudaError_t launch_behind(bool behind, void (*kernel)(Params...), dim3 grid, int block, size_t smem, cudaStream_t st,
+                          Args... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(block);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr = {};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = behind ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
 template <int D, bool F16>
@@ -1466,8 +1537,7 @@ nabla_status launch(const AttnParams& p, const nabla_cache& cache, uint32_t* sta
     if (e != cudaSuccess) return cuda_status(e);
   }
   if (a.few0 > 0) {
-    prefix_attn_kernel<D, F16><<<ctas, kThreads, C::kSmemBytes, st>>>(mk, mv, a);
-    e = cudaGetLastError();
+    e = launch_behind(a.few1 > a.few0, prefix_attn_kernel<D, F16>, dim3(ctas), kThreads, C::kSmemBytes, st, mk, mv, a);
     if (e != cudaSuccess) return cuda_status(e);
   }
   dim3 grid(ctas, kJoinBlocks);
@@ -1475,8 +1545,7 @@ nabla_status launch(const AttnParams& p, const nabla_cache& cache, uint32_t* sta
     const long long blocks = (static_cast<long long>(a.Hkv) * a.B * a.R + kJoinRows - 1) / kJoinRows;
     grid = dim3(static_cast<unsigned>(blocks < 1 << 20 ? blocks : 1 << 20));
   }
-  prefix_join_kernel<D, F16><<<grid, kJoinThreads, 0, st>>>(a, status, ctas, few_ctas);
-  return cuda_status(cudaGetLastError());
+  return cuda_status(launch_behind(true, prefix_join_kernel<D, F16>, grid, kJoinThreads, 0, st, a, status, ctas, few_ctas));
 }
 
 }  // namespace
@@ -1582,7 +1651,7 @@ extern "C" nabla_status nabla_prefix_attn(nabla_heads q, int32_t B, int32_t Sq, 
   // without tails (or without a prefix) shared mode has only the other kind of items
   p.n_prefix = plan.shared && (prefix_len > 0 || !tail_pages) ? static_cast<int>(plan.n_prefix) : 0;
   p.n_items = plan.shared ? p.n_prefix + (tail_pages ? static_cast<int>(plan.n_tail) : 0) : static_cast<int>(plan.n_items);
-  p.tail_half = p.R < 128 ? p.R : 128;
+  p.tail_rows = p.R <= 128 ? p.R : kRows;
   p.few0 = !plan.few_tail ? p.n_items : (plan.few_prefix ? 0 : p.n_prefix);
   p.few1 = p.n_items;
   char* ws = static_cast<char*>(workspace);
