@@ -1,7 +1,8 @@
 """Thin Python binding of the NABLA C ABI (``include/nabla.h``) for torch tensors.
 
-Argument marshalling only: every step of the hot path runs in ``libnabla.so``'s CUDA
-kernels.  torch is used for device memory and streams.  Functions carry the C names:
+Argument marshalling only (ctypes; for the calls that serve single tokens the native module
+``_binding.so``): every step of the hot path runs in ``libnabla.so``'s CUDA kernels.  torch
+is used for device memory and streams.  Functions carry the C names:
 
   nabla_reorder, nabla_build_mask, nabla_mask_lists, nabla_attn_fwd, nabla_attn_bwd,
   nabla_mask_workspace_bytes, nabla_fwd_workspace_bytes, nabla_bwd_workspace_bytes,
@@ -396,56 +397,21 @@ NABLA_ROPE_PARTS = 3
 DEVICE_BAD_PAGE = 0x301
 DEVICE_BAD_LENGTH = 0x302
 
-_ABSENT = _Heads()
+_native = None
 
 
-def _heads(t, B, S, D, what):
-    """The [B, H, S, D] view of a tensor, strides included."""
-    shape = t.shape
-    if len(shape) != 4 or shape[0] != B or shape[2] != S or shape[3] != D:
-        raise ValueError(f"{what}: expected [{B}, H, {S}, {D}], got {tuple(shape)}")
-    sb, sh, ss, sd = t.stride()
-    if sd != 1:
-        raise ValueError(f"{what}: the last dimension must be contiguous")
-    return _Heads(t.data_ptr(), dtype_code(t), shape[1], sb, sh, ss)
-
-
-def _int_table(t, shape, what):
-    """Pointer of a contiguous int32 tensor of the given shape (None stays None)."""
-    if t is None:
-        return None
-    if t.dtype is not torch.int32 or t.shape != shape or not t.is_contiguous():
-        raise ValueError(f"{what}: expected a contiguous int32 tensor {shape}, got {t.dtype} {tuple(t.shape)}")
-    return t.data_ptr()
-
-
-def _same_device(device, tensors, names):
-    if device.type != "cuda":
-        raise ValueError(f"expected CUDA tensors, got {device}")
-    for i, t in enumerate(tensors):
-        if t is not None and t.device != device:
-            raise ValueError(f"{names.split()[i]} is on {t.device}, the call on {device}")
-
-
-def _launch(device, stream, where, fn, *args):
-    """fn(*args, stream pointer) with the tensors' device current (a stream of that device)."""
-    index = device.index
-    st = torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
-    if torch.cuda.current_device() == index:
-        rc = fn(*args, st)
-    else:
-        with torch.cuda.device(device):
-            rc = fn(*args, st)
-    if rc != NABLA_OK:
-        raise NablaError(rc, where)
-
-
-def _empty_like(t, dtype, stream):
-    """Contiguous memory of t's shape, owned by the stream that will use it."""
-    if stream is None:
-        return torch.empty_like(t, dtype=dtype, memory_format=torch.contiguous_format)
-    with torch.cuda.stream(stream):
-        return torch.empty_like(t, dtype=dtype, memory_format=torch.contiguous_format)
+def _load_binding():
+    """Import ``_binding.so`` (once); raises if it has not been built."""
+    global _native
+    if _native is None:
+        load_library()
+        try:
+            from . import _binding as b
+        except ImportError as e:
+            raise ImportError(f"_binding.so cannot be loaded ({e}); run "
+                              "`python -m adaptive_block_sparse_b200.build`") from e
+        _native = b
+    return _native
 
 
 class Rope:
@@ -455,16 +421,20 @@ class Rope:
     ``axis_dims``: rotated channels of the (t, h, w) axes, or None for one axis.
     """
 
-    __slots__ = ("inv_freq", "axes", "c")
+    __slots__ = ("args",)
 
     def __init__(self, inv_freq, style=NABLA_ROPE_INTERLEAVED, axis_dims=None, magnitude=1.0):
-        if inv_freq.dtype is not torch.float64 or inv_freq.dim() != 1 or not inv_freq.is_contiguous():
+        if inv_freq.dtype is not torch.float64 or inv_freq.dim() != 1:
             raise ValueError("inv_freq: expected a contiguous fp64 vector")
-        self.inv_freq = inv_freq
-        self.axes = 1 if axis_dims is None else 3
-        dim = 2 * inv_freq.shape[0]
-        t, h, w = (dim, 0, 0) if axis_dims is None else axis_dims
-        self.c = _Rope(style, dim, self.axes, t, h, w, magnitude, inv_freq.data_ptr())
+        if axis_dims is None:
+            self.args = (inv_freq, style, 1, 2 * len(inv_freq), 0, 0, magnitude)
+        else:
+            t, h, w = axis_dims
+            self.args = (inv_freq, style, 3, t, h, w, magnitude)
+
+    @property
+    def inv_freq(self):
+        return self.args[0]
 
     @classmethod
     def build(cls, dim, device, style=NABLA_ROPE_INTERLEAVED, axis_dims=None, base=10000.0,
@@ -500,43 +470,15 @@ def nabla_rotary(q, k, rope: Rope, grid=None, positions=None, origin=(0, 0, 0), 
     [B, S] or [B, S, axes] instead of the grid's.  ``adjoint`` maps the gradients of the
     outputs to those of the inputs.  Returns (q_out, k_out), contiguous unless given.
     """
-    x = q if q is not None else k
-    B, _, S, D = x.shape
-    device = x.device
-    _same_device(device, (k, q_out, k_out, positions, rope.inv_freq), "k q_out k_out positions inv_freq")
-    if grid is None:
-        grid = (S, 1, 1)
-    elif grid[0] * grid[1] * grid[2] != S:
-        raise ValueError(f"grid {tuple(grid)} does not hold {S} tokens")
-    qs = qd = ks = kd = _ABSENT
-    if q is not None:
-        if q_out is None:
-            q_out = _empty_like(q, out_dtype, stream)
-        qs, qd = _heads(q, B, S, D, "q"), _heads(q_out, B, S, D, "q_out")
-    elif q_out is not None:
-        raise ValueError("q_out without q")
-    if k is not None:
-        if k_out is None:
-            k_out = _empty_like(k, out_dtype, stream)
-        ks, kd = _heads(k, B, S, D, "k"), _heads(k_out, B, S, D, "k_out")
-    elif k_out is not None:
-        raise ValueError("k_out without k")
-    pos = None
-    if positions is not None:
-        pos = _int_table(positions, (B, S) if positions.dim() == 2 and rope.axes == 1 else (B, S, rope.axes),
-                         "positions")
-    _launch(device, stream, "nabla_rotary", load_library().nabla_rotary, qs, qd, ks, kd, B, _Grid(*grid), D,
-            rope.c, _Grid(*origin), pos, src_layout, dst_layout, int(adjoint))
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return nabla_rotary(q, k, rope, grid, positions, origin, q_out, k_out, out_dtype, src_layout,
+                                dst_layout, adjoint)
+    rc, q_out, k_out = (_native or _load_binding()).rotary(q, k, q_out, k_out, rope.args, grid, origin, positions,
+                                                            out_dtype, src_layout, dst_layout, int(adjoint))
+    if rc:
+        raise NablaError(rc, "nabla_rotary")
     return q_out, k_out
-
-
-def _cache(k_cache, v_cache):
-    if k_cache.dim() != 4 or k_cache.shape != v_cache.shape or k_cache.dtype != v_cache.dtype:
-        raise ValueError("k_cache and v_cache: expected two [pages, H, page, D] pools of one shape and dtype")
-    if not (k_cache.is_contiguous() and v_cache.is_contiguous()):
-        raise ValueError("k_cache and v_cache must be contiguous")
-    n, H, page, D = k_cache.shape
-    return _Cache(k_cache.data_ptr(), v_cache.data_ptr(), n, H, page, D, dtype_code(k_cache))
 
 
 def nabla_cache_append(k, v, k_cache, v_cache, page_table, start, rope: Rope = None, frame=(1, 1), pos0=0,
@@ -546,51 +488,20 @@ def nabla_cache_append(k, v, k_cache, v_cache, page_table, start, rope: Rope = N
     rotate it in the same launch.  ``frame``: (Hg, W) of a latent frame for three axes.
     ``status``: uint8 or int32 CUDA tensor of at least 4 zeroed bytes for
     ``nabla_read_device_status``.  Returns q_out (None without q)."""
-    B, _, S, D = k.shape
-    device = k.device
-    _same_device(device, (v, k_cache, v_cache, page_table, start, positions, counts, q, q_out, status,
-                          rope.inv_freq if rope is not None else None),
-                 "v k_cache v_cache page_table start positions counts q q_out status inv_freq")
-    cache = _cache(k_cache, v_cache)
-    qs = qd = _ABSENT
-    if q is not None:
-        if q_out is None:
-            q_out = _empty_like(q, None, stream)
-        qs, qd = _heads(q, B, S, D, "q"), _heads(q_out, B, S, D, "q_out")
-    elif q_out is not None:
-        raise ValueError("q_out without q")
-    if D != k_cache.shape[3]:
-        raise ValueError(f"k has rows of {D}, the cache of {k_cache.shape[3]}")
-    if page_table.dim() != 2:
-        raise ValueError("page_table: expected [B, pages]")
-    width = page_table.shape[1]
-    pos = None
-    if positions is not None:
-        if rope is None:
-            raise ValueError("positions without rope")
-        pos = _int_table(positions, (B, S) if positions.dim() == 2 and rope.axes == 1 else (B, S, rope.axes),
-                         "positions")
-    if status is not None and status.numel() * status.element_size() < 4:
-        raise ValueError("status: expected at least 4 bytes")
-    _launch(device, stream, "nabla_cache_append", load_library().nabla_cache_append,
-            _heads(k, B, S, D, "k"), _heads(v, B, S, D, "v"), qs, qd, B, S, cache,
-            _int_table(page_table, (B, width), "page_table"), width, _int_table(start, (B,), "start"),
-            _int_table(counts, (B,), "counts"), ctypes.byref(rope.c) if rope is not None else None,
-            _Grid(0, *frame), pos0, pos, None if status is None else status.data_ptr())
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return nabla_cache_append(k, v, k_cache, v_cache, page_table, start, rope, frame, pos0, positions,
+                                      counts, q, q_out, status)
+    rc, q_out = (_native or _load_binding()).append(k, v, k_cache, v_cache, page_table, start,
+                                                     None if rope is None else rope.args, frame, pos0, positions,
+                                                     counts, q, q_out, status)
+    if rc:
+        raise NablaError(rc, "nabla_cache_append")
     return q_out
 
 
 def nabla_prefix_workspace_bytes(B, Hq, Hkv, Sq, D) -> int:
     return int(load_library().nabla_prefix_workspace_bytes(B, Hq, Hkv, Sq, D))
-
-
-def _f32_rows(t, B, H, S, what):
-    """Pointer of a contiguous f32 [B, H, S] tensor (None stays None)."""
-    if t is None:
-        return None
-    if t.dtype is not torch.float32 or t.shape != (B, H, S) or not t.is_contiguous():
-        raise ValueError(f"{what}: expected a contiguous f32 tensor {(B, H, S)}, got {t.dtype} {tuple(t.shape)}")
-    return t.data_ptr()
 
 
 def nabla_prefix_attn(q, k_cache, v_cache, prefix_pages, prefix_len, tail_pages=None, tail_len=None, q_len=None,
@@ -601,43 +512,15 @@ def nabla_prefix_attn(q, k_cache, v_cache, prefix_pages, prefix_len, tail_pages=
     ``tail_pages[b]``; ``part_o`` / ``part_lse`` merge a result over other keys (the
     block-sparse forward's O and LSE).  Returns (o, lse); ``lse`` is written when given.  The
     first word of ``workspace`` receives the device status (``nabla_read_device_status``)."""
-    B, Hq, Sq, D = q.shape
-    device = q.device
-    _same_device(device, (k_cache, v_cache, prefix_pages, tail_pages, tail_len, q_len, part_o, part_lse, o, lse,
-                          workspace),
-                 "k_cache v_cache prefix_pages tail_pages tail_len q_len part_o part_lse o lse workspace")
-    cache = _cache(k_cache, v_cache)
-    if cache.D != D:
-        raise ValueError(f"q has rows of {D}, the cache of {cache.D}")
-    if o is None:
-        o = _empty_like(q, o_dtype, stream)
-    lib = load_library()
-    if workspace is None:
-        need = lib.nabla_prefix_workspace_bytes(B, Hq, cache.H, Sq, D)
-        if stream is None:
-            workspace = torch.empty(need, dtype=torch.uint8, device=device)
-        else:
-            with torch.cuda.stream(stream):
-                workspace = torch.empty(need, dtype=torch.uint8, device=device)
-    elif workspace.dtype is not torch.uint8 or not workspace.is_contiguous():
-        raise ValueError("workspace: expected a contiguous uint8 tensor")
-    n_prefix = 0
-    if prefix_pages is not None:
-        n_prefix = prefix_pages.shape[0]
-        if n_prefix * cache.page < prefix_len:
-            raise ValueError(f"{n_prefix} pages of {cache.page} do not hold a prefix of {prefix_len}")
-    width = 0
-    if tail_pages is not None:
-        if tail_pages.dim() != 2:
-            raise ValueError("tail_pages: expected [B, pages]")
-        width = tail_pages.shape[1]
-    _launch(device, stream, "nabla_prefix_attn", lib.nabla_prefix_attn, _heads(q, B, Sq, D, "q"), B, Sq, cache,
-            _int_table(prefix_pages, (n_prefix,), "prefix_pages"), prefix_len,
-            _int_table(tail_pages, (B, width), "tail_pages"), width, _int_table(tail_len, (B,), "tail_len"),
-            _int_table(q_len, (B,), "q_len"), int(causal), 1.0 / math.sqrt(D) if scale is None else scale,
-            _ABSENT if part_o is None else _heads(part_o, B, Sq, D, "part_o"),
-            _f32_rows(part_lse, B, Hq, Sq, "part_lse"), _heads(o, B, Sq, D, "o"),
-            _f32_rows(lse, B, Hq, Sq, "lse"), workspace.data_ptr(), workspace.numel())
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return nabla_prefix_attn(q, k_cache, v_cache, prefix_pages, prefix_len, tail_pages, tail_len, q_len,
+                                     causal, scale, part_o, part_lse, o, o_dtype, lse, workspace)
+    rc, o = (_native or _load_binding()).prefix_attn(q, k_cache, v_cache, prefix_pages, prefix_len, tail_pages,
+                                                      tail_len, q_len, causal, scale, part_o, part_lse, o, o_dtype,
+                                                      lse, workspace)
+    if rc:
+        raise NablaError(rc, "nabla_prefix_attn")
     return o, lse
 
 

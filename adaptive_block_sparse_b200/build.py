@@ -4,6 +4,8 @@ Usage: ``python -m adaptive_block_sparse_b200.build`` (or ``build()`` from Pytho
 Each ``csrc/*.cu`` is compiled in parallel to an object file under ``_build/``; the
 objects are linked into ``adaptive_block_sparse_b200/libnabla.so`` with the CUDA runtime
 linked statically, so the library depends only on the NVIDIA driver at run time.
+``csrc/binding.cpp`` (argument marshalling from torch tensors, host code) is compiled against
+the installed torch into the Python module ``_binding.so`` beside it.
 """
 
 from __future__ import annotations
@@ -13,6 +15,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -20,6 +23,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libnabla.so")
+BINDING_SRC = os.path.join(CSRC, "binding.cpp")
+BINDING = os.path.join(PKG, "_binding.so")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I", INCLUDE,
@@ -58,12 +63,53 @@ def _compile(src: str, verbose: bool, extra) -> str:
     return obj
 
 
+def _run(cmd, what, verbose):
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        raise RuntimeError(f"{what} failed:\n{res.stdout}\n{res.stderr}")
+
+
+def _torch_dir() -> str:
+    import torch
+    return os.path.dirname(os.path.abspath(torch.__file__))
+
+
+def _compile_binding(verbose: bool) -> str:
+    obj = os.path.join(BUILD, "binding.cpp.o")
+    deps = [BINDING_SRC, os.path.join(INCLUDE, "nabla.h"), os.path.join(_torch_dir(), "version.py")]
+    if os.path.exists(obj) and os.path.getmtime(obj) >= max(os.path.getmtime(p) for p in deps):
+        return obj
+    import torch
+    inc = os.path.join(_torch_dir(), "include")
+    cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc()))), "include")
+    _run(["g++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden",
+          f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I", INCLUDE, "-isystem", inc,
+          "-isystem", os.path.join(inc, "torch", "csrc", "api", "include"), "-isystem", cuda,
+          "-isystem", sysconfig.get_paths()["include"], "-c", BINDING_SRC, "-o", obj], "binding.cpp", verbose)
+    return obj
+
+
+def _link_binding(obj: str, verbose: bool) -> None:
+    if os.path.exists(BINDING) and os.path.getmtime(BINDING) >= os.path.getmtime(obj):
+        return
+    lib = os.path.join(_torch_dir(), "lib")
+    tmp = BINDING + ".tmp"
+    _run(["g++", "-shared", "-o", tmp, obj, "-L", PKG, "-l:libnabla.so", "-L", lib, "-ltorch_python", "-ltorch",
+          "-ltorch_cpu", "-lc10", "-lc10_cuda", f"-Wl,-rpath,$ORIGIN,-rpath,{lib}"], "linking the binding", verbose)
+    os.replace(tmp, BINDING)
+
+
 def build(verbose: bool = False, extra=()) -> str:
-    """Compile every CUDA source and link ``libnabla.so``; returns its path."""
+    """Compile every CUDA source, link ``libnabla.so`` and build ``_binding.so``; returns the
+    library's path."""
     os.makedirs(BUILD, exist_ok=True)
     srcs = _sources()
-    with cf.ThreadPoolExecutor(max_workers=min(8, len(srcs))) as ex:
+    with cf.ThreadPoolExecutor(max_workers=min(8, len(srcs) + 1)) as ex:
+        binding = ex.submit(_compile_binding, verbose)
         objs = list(ex.map(lambda s: _compile(s, verbose, list(extra)), srcs))
+        binding_obj = binding.result()
     if (not os.path.exists(LIB) or extra or
             os.path.getmtime(LIB) < max(os.path.getmtime(o) for o in objs)):
         tmp = LIB + ".tmp"
@@ -75,6 +121,7 @@ def build(verbose: bool = False, extra=()) -> str:
         if res.returncode != 0:
             raise RuntimeError(f"link failed:\n{res.stdout}\n{res.stderr}")
         os.replace(tmp, LIB)
+    _link_binding(binding_obj, verbose)
     return LIB
 
 

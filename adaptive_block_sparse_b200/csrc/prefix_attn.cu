@@ -35,6 +35,8 @@
 // 0 * NaN would reach O); scores past a length are replaced by -inf.
 #include <math.h>
 
+#include <atomic>
+
 #include <cudaTypedefs.h>
 
 #include "history.cuh"
@@ -1506,32 +1508,71 @@ cudaError_t launch_behind(bool behind, void (*kernel)(Params...), dim3 grid, int
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
+// What a launch needs to know of the current device, looked up once per context (a device
+// reset gives a new context id): SMs, and that the kernels' shared memory was allowed.
+constexpr int kMaxDevices = 64;
+
+bool current_context_id(unsigned long long* id) {
+  static std::atomic<PFN_cuCtxGetCurrent_v4000> get_current{nullptr};
+  static std::atomic<PFN_cuCtxGetId_v12000> get_id{nullptr};
+  if (get_id.load() == nullptr) {
+    void *a = nullptr, *b = nullptr;
+    cudaDriverEntryPointQueryResult r1, r2;
+    if (cudaGetDriverEntryPoint("cuCtxGetCurrent", &a, cudaEnableDefault, &r1) != cudaSuccess ||
+        r1 != cudaDriverEntryPointSuccess ||
+        cudaGetDriverEntryPoint("cuCtxGetId", &b, cudaEnableDefault, &r2) != cudaSuccess ||
+        r2 != cudaDriverEntryPointSuccess)
+      return false;
+    get_current.store(reinterpret_cast<PFN_cuCtxGetCurrent_v4000>(a));
+    get_id.store(reinterpret_cast<PFN_cuCtxGetId_v12000>(b));
+  }
+  CUcontext ctx = nullptr;
+  *id = 0;
+  return get_current.load()(&ctx) == CUDA_SUCCESS && (ctx == nullptr || get_id.load()(ctx, id) == CUDA_SUCCESS);
+}
+
+template <int D, bool F16>
+nabla_status set_up(int* sms) {
+  static std::atomic<unsigned long long> ready[kMaxDevices];   // context id + 1
+  static std::atomic<int> n_sms[kMaxDevices];
+  int dev = -1;
+  unsigned long long id = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || !current_context_id(&id)) return NABLA_ERR_CUDA;
+  if (dev >= kMaxDevices) return NABLA_ERR_UNSUPPORTED;
+  if (id == 0 || ready[dev].load() != id + 1) {
+    int n = 0;
+    cudaFuncAttributes fa;
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
+        cudaFuncSetAttribute(prefix_attn_kernel<D, F16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             Cfg<D>::kSmemBytes) != cudaSuccess ||
+        cudaFuncSetAttribute(rows_attn_kernel<D, F16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             FewCfg<D>::kSmemBytes) != cudaSuccess ||
+        cudaFuncGetAttributes(&fa, prefix_attn_kernel<D, F16>) != cudaSuccess)
+      return NABLA_ERR_CUDA;
+    // The register split needs the block to launch with kLaunchRegs a thread.
+    if (fa.numRegs != kLaunchRegs) return NABLA_ERR_UNSUPPORTED;
+    n_sms[dev].store(n);
+    if (id != 0)   // (0: no context was current yet; the next call notes it)
+      ready[dev].store(id + 1);
+  }
+  *sms = n_sms[dev].load();
+  return NABLA_OK;
+}
+
 template <int D, bool F16>
 nabla_status launch(const AttnParams& p, const nabla_cache& cache, uint32_t* status, cudaStream_t st) {
   using C = Cfg<D>;
-  int dev = 0, sms = kMaxCtas;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  if (e != cudaSuccess) return cuda_status(e);
+  int sms = 0;
+  nabla_status rc = set_up<D, F16>(&sms);
+  if (rc != NABLA_OK) return rc;
   const int ctas = sms < kMaxCtas ? sms : kMaxCtas, few_ctas = 2 * ctas;
   AttnParams a = p;
   a.whole = a.shared ? 0 : a.n_items / ctas;
   CUtensorMap mk, mv;
-  if (a.few0 > 0) {
-    if (!make_map_pool(&mk, cache.k, cache) || !make_map_pool(&mv, cache.v, cache)) return NABLA_ERR_CUDA;
-    e = cudaFuncSetAttribute(prefix_attn_kernel<D, F16>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
-    if (e != cudaSuccess) return cuda_status(e);
-    // The register split needs the block to launch with kLaunchRegs a thread.
-    cudaFuncAttributes fa;
-    e = cudaFuncGetAttributes(&fa, prefix_attn_kernel<D, F16>);
-    if (e != cudaSuccess) return cuda_status(e);
-    if (fa.numRegs != kLaunchRegs) return NABLA_ERR_UNSUPPORTED;
-  }
+  if (a.few0 > 0 && (!make_map_pool(&mk, cache.k, cache) || !make_map_pool(&mv, cache.v, cache))) return NABLA_ERR_CUDA;
+  cudaError_t e;
   if (a.few1 > a.few0) {
-    using F = FewCfg<D>;
-    e = cudaFuncSetAttribute(rows_attn_kernel<D, F16>, cudaFuncAttributeMaxDynamicSharedMemorySize, F::kSmemBytes);
-    if (e != cudaSuccess) return cuda_status(e);
-    rows_attn_kernel<D, F16><<<few_ctas, kFewThreads, F::kSmemBytes, st>>>(
+    rows_attn_kernel<D, F16><<<few_ctas, kFewThreads, FewCfg<D>::kSmemBytes, st>>>(
         static_cast<const uint16_t*>(cache.k), static_cast<const uint16_t*>(cache.v), a);
     e = cudaGetLastError();
     if (e != cudaSuccess) return cuda_status(e);
