@@ -137,6 +137,11 @@ CASES = {
     "causal empty rows": dict(B=2, Hq=2, Hkv=2, D=64, Sq=6, P=0, tails=[3, 0], page=16, causal=True),
     "causal into the prefix": dict(B=2, Hq=2, Hkv=2, D=128, Sq=9, P=131, tails=[3, 0], page=16, causal=True),
     "many rows": dict(B=30, Hq=12, Hkv=2, D=128, Sq=3, P=700, tails=list(range(0, 300, 10)), page=64),
+    "few rows wide": dict(B=3, Hq=12, Hkv=2, D=128, Sq=3, P=700, tails=[0, 31, 300], page=16),
+    "wide tails": dict(B=5, Hq=6, Hkv=2, D=64, Sq=11, P=260, tails=[11, 12, 0, 130, 300], page=64, causal=True,
+                       q_len=[11, 5, 0, 11, 3], dtype=F16),
+    "wide prefix alone": dict(B=33, Hq=1, Hkv=1, D=128, Sq=1, P=1111, tails=None, page=32),
+    "alternate slots": dict(B=2, Hq=2, Hkv=2, D=64, Sq=70, P=900, tails=[70, 333], page=32, causal=True),
     "dual tails": dict(B=3, Hq=10, Hkv=2, D=128, Sq=40, P=300, tails=[400, 0, 77], page=64, q_len=[40, 0, 33]),
     "ragged causal": dict(B=4, Hq=4, Hkv=2, D=128, Sq=60, P=100, tails=[90, 60, 0, 17], page=16, causal=True,
                           q_len=[60, 1, 0, 17], dtype=F16),
