@@ -1259,14 +1259,148 @@ __global__ void __launch_bounds__(kFewThreads, 2) rows_attn_kernel(const uint16_
   }
 }
 
-// Joins the parts of split items, merges the caller's part and writes the rows; block 0
-// also gathers the CTAs' status words and looks the lengths over.  Four warps share a row: a
-// long prefix leaves a row up to two parts per CTA, which are read in parallel (every fourth
-// part by one warp, always the same ones, so results do not depend on timing).
+// Joining the parts of split items, merging the caller's part and writing the rows; block 0
+// also gathers the CTAs' status words and looks the lengths over.
 constexpr int kJoinThreads = 256;
+
+__device__ __forceinline__ void gather_status(const AttnParams& p, uint32_t* status, int ctas, int few_ctas) {
+  const int lane = threadIdx.x & 31;
+  uint32_t w = 0;
+  for (int c = lane; c < kMaxCtas + kRowCtas; c += 32) {
+    // the words of the kernels that ran
+    const bool ran = c < kMaxCtas ? p.few0 > 0 && c < ctas : p.few1 > p.few0 && c < kMaxCtas + few_ctas;
+    if (ran && w == 0) w = p.cta_status[c];
+  }
+  for (int i = lane; i < p.B; i += 32) {
+    if (p.q_len != nullptr && queries_of(p, i) != p.q_len[i] && w == 0) w = kDevBadLength;
+    if (p.tail_pages != nullptr && tail_of(p, i) != p.tail_len[i] && w == 0) w = kDevBadLength;
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    const uint32_t v = __shfl_xor_sync(0xffffffffu, w, o);
+    if (w == 0) w = v;
+  }
+  if (lane == 0) *status = w;
+}
+
+// Own mode: many rows with few parts each.  A warp joins eight rows at a time, four lanes a
+// row for the log-sums (four parts at a time), then all lanes for a row's channels.  Bound by
+// the latency of its loads.
+constexpr int kOwnJoinBlocks = kRows / 64;
+template <int D, bool F16>
+__global__ void __launch_bounds__(kJoinThreads) own_join_kernel(const __grid_constant__ AttnParams p, uint32_t* status,
+                                                                int ctas) {
+  constexpr int kPer = D / 32;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  wait_for_kernel_before();
+  if (blockIdx.x == 0 && blockIdx.y == 0 && warp == 0) gather_status(p, status, ctas, 0);
+  const int i = p.cta_done[blockIdx.x];
+  if (i < 0) return;
+  const Item t = item_of(p, i);
+  const int first = p.first[i - p.whole * ctas], last = p.last[i - p.whole * ctas];
+  if (first < 0 || last < first || last >= ctas) return;       // only after a wait gave up
+  const int n = last - first + 1, row0 = blockIdx.y * 64 + warp * 8;
+  if (row0 >= t.rows) return;
+  const int mine = row0 + (lane >> 2);       // the row of this lane's group of four
+  int gh = 0;
+  const int s = mine < t.rows ? p.div_g.div(t.row0 + mine, &gh) : 0;
+  const bool live = mine < t.rows && s < queries_of(p, t.b);
+  // workspace row of part j of item row r: part_row(...) + r
+  auto base_of = [&](int j) { return part_row(p, i, first + j, j > 0, 0, 0); };
+  float m = -INFINITY, sum = 0.f;
+  bool nan = false;
+  float acc[8][kPer];
+#pragma unroll
+  for (int r = 0; r < 8; ++r)
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) acc[r][k] = 0.f;
+  for (int jc = 0; jc < n; jc += 4) {
+    const int j = jc + (lane & 3);
+    const float v = live && j < n ? p.part_l[base_of(j) + mine] : -INFINITY;
+    nan |= v != v;
+    float top = v;
+    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+    top = fmaxf(top, m);
+    const float f = m == -INFINITY ? 0.f : exp2f(m - top);
+    float e = v == -INFINITY || top == -INFINITY ? 0.f : exp2f(v - top);
+    float es = e;
+    es += __shfl_xor_sync(0xffffffffu, es, 1);
+    es += __shfl_xor_sync(0xffffffffu, es, 2);
+    sum = sum * f + es;
+    m = top;
+#pragma unroll
+    for (int r = 0; r < 8; ++r) {
+      const float fr = __shfl_sync(0xffffffffu, f, 4 * r);
+#pragma unroll
+      for (int k = 0; k < kPer; ++k) acc[r][k] *= fr;
+    }
+#pragma unroll
+    for (int jj = 0; jj < 4; ++jj) {
+      if (jc + jj >= n) break;
+      const float* src = p.part_acc + (base_of(jc + jj) + row0) * D + lane * kPer;
+      float x[8][kPer], w[8];
+#pragma unroll
+      for (int r = 0; r < 8; ++r) {
+        w[r] = __shfl_sync(0xffffffffu, e, 4 * r + jj);
+#pragma unroll
+        for (int k = 0; k < kPer; k += 2) {
+          const float2 y = w[r] != 0.f ? *reinterpret_cast<const float2*>(src + r * D + k) : make_float2(0.f, 0.f);
+          x[r][k] = y.x;
+          x[r][k + 1] = y.y;
+        }
+      }
+#pragma unroll
+      for (int r = 0; r < 8; ++r)
+#pragma unroll
+        for (int k = 0; k < kPer; ++k) acc[r][k] += w[r] * x[r][k];
+    }
+  }
+  nan |= __shfl_xor_sync(0xffffffffu, static_cast<int>(nan), 1) != 0;
+  nan |= __shfl_xor_sync(0xffffffffu, static_cast<int>(nan), 2) != 0;
+  float lse2 = sum > 0.f ? m + log2f(sum) : -INFINITY;
+  float wa = sum > 0.f ? 1.f / sum : 0.f, wb = 0.f;
+  if (nan) lse2 = wa = __int_as_float(0x7FC00000);
+  const int h = t.kvh * p.G + gh;
+  const long long flat = (static_cast<long long>(t.b) * p.Hq + h) * p.Sq + s;
+  if (p.part_lse != nullptr && live) {
+    const float a = p.part_lse[flat] * 1.4426950408889634f;
+    if (a != -INFINITY) {
+      const float both = join(lse2, a);
+      wa *= lse2 == -INFINITY ? 0.f : exp2f(lse2 - both);
+      wb = exp2f(a - both);
+      lse2 = both;
+    }
+  }
+  __syncwarp();        // every lane has read part_lse, which may be lse
+  if (p.lse != nullptr && live && (lane & 3) == 0) p.lse[flat] = lse2 * 0.69314718055994531f;
+  const long long to = t.b * p.o_b + h * p.o_h + s * p.o_s, from = t.b * p.po_b + h * p.po_h + s * p.po_s;
+#pragma unroll
+  for (int r = 0; r < 8; ++r) {
+    const bool go = __shfl_sync(0xffffffffu, static_cast<int>(live), 4 * r) != 0;
+    const float a = __shfl_sync(0xffffffffu, wa, 4 * r), b = __shfl_sync(0xffffffffu, wb, 4 * r);
+    const long long off = __shfl_sync(0xffffffffu, to, 4 * r) + lane * kPer;
+    const long long poff = __shfl_sync(0xffffffffu, from, 4 * r) + lane * kPer;
+    if (!go) continue;
+#pragma unroll
+    for (int k = 0; k < kPer; k += 2) {
+      float2 y = make_float2(0.f, 0.f);
+      if (b != 0.f) {
+        if (p.part_f32) y = *reinterpret_cast<const float2*>(static_cast<const float*>(p.part_o) + poff + k);
+        else y = unpack2<F16>(*reinterpret_cast<const uint32_t*>(static_cast<const uint16_t*>(p.part_o) + poff + k));
+      }
+      const float u = acc[r][k] * a + y.x * b, v = acc[r][k + 1] * a + y.y * b;
+      if (p.o_f32) *reinterpret_cast<float2*>(static_cast<float*>(p.o) + off + k) = make_float2(u, v);
+      else *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.o) + off + k) = pack2<F16>(u, v);
+    }
+  }
+}
+
+// Shared mode.  Four warps share a row: a long prefix leaves a row a part in every CTA, and
+// they are read in parallel (every fourth part by one warp, always the same ones, so results
+// do not depend on timing).
 constexpr int kRowWarps = 4;
 constexpr int kJoinRows = kJoinThreads / 32 / kRowWarps;     // rows at a time
-constexpr int kJoinBlocks = 16;                              // blocks per split item (own mode)
 
 // Parts of one item that hold a row: the first in workspace row r0, part j > 0 in r1 +
 // (j - 1) step.
@@ -1279,8 +1413,7 @@ struct PartList {
 
 __device__ __forceinline__ PartList parts_of(const AttnParams& p, int i, int lrow, int ctas) {
   PartList l;
-  const int e = i - p.whole * ctas;
-  const int first = p.first[e], last = p.last[e];
+  const int first = p.first[i], last = p.last[i];
   l.n = 0;
   const bool few = i >= p.few0 && i < p.few1;
   if (first < 0 || last < first || last >= (few ? kRowCtas : ctas)) return l;       // only after a wait gave up
@@ -1293,15 +1426,9 @@ __device__ __forceinline__ PartList parts_of(const AttnParams& p, int i, int lro
   }
   const int half = lrow >> 7, row = lrow & 127;
   l.r0 = part_row(p, i, first, false, half, row);
-  if (!p.shared) {
-    l.n = last - first + 1;
-    l.r1 = part_row(p, i, first + 1, true, half, row);
-    l.step = 4 * 128;
-  } else {
-    l.n = last - first + 1;
-    l.step = i < p.n_prefix ? kRows : p.tail_rows;
-    l.r1 = l.r0 + l.step;
-  }
+  l.n = last - first + 1;
+  l.step = i < p.n_prefix ? kRows : p.tail_rows;
+  l.r1 = l.r0 + l.step;
   return l;
 }
 
@@ -1312,40 +1439,10 @@ __global__ void __launch_bounds__(kJoinThreads) prefix_join_kernel(const __grid_
   __shared__ float acc_s[kJoinRows][kRowWarps][D];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   wait_for_kernel_before();
-  if (blockIdx.x == 0 && blockIdx.y == 0 && warp == 0) {
-    uint32_t w = 0;
-    for (int c = lane; c < kMaxCtas + kRowCtas; c += 32) {
-      // the words of the kernels that ran
-      const bool ran = c < kMaxCtas ? p.few0 > 0 && c < ctas : p.few1 > p.few0 && c < kMaxCtas + few_ctas;
-      if (ran && w == 0) w = p.cta_status[c];
-    }
-    for (int i = lane; i < p.B; i += 32) {
-      if (p.q_len != nullptr && queries_of(p, i) != p.q_len[i] && w == 0) w = kDevBadLength;
-      if (p.tail_pages != nullptr && tail_of(p, i) != p.tail_len[i] && w == 0) w = kDevBadLength;
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      const uint32_t v = __shfl_xor_sync(0xffffffffu, w, o);
-      if (w == 0) w = v;
-    }
-    if (lane == 0) *status = w;
-  }
+  if (blockIdx.x == 0 && warp == 0) gather_status(p, status, ctas, few_ctas);
   const int slot = warp / kRowWarps, sub = warp % kRowWarps;
-  // this block's rows: of the whole call (shared mode), or of the item that CTA blockIdx.x
-  // completed
-  int item = -1;
-  Item t;
-  long long n_rows, row0 = static_cast<long long>(blockIdx.y) * kJoinRows, stride = kJoinBlocks * kJoinRows;
-  if (p.shared) {
-    n_rows = static_cast<long long>(p.Hkv) * p.B * p.R;
-    row0 = static_cast<long long>(blockIdx.x) * kJoinRows;
-    stride = static_cast<long long>(gridDim.x) * kJoinRows;
-  } else {
-    item = p.cta_done[blockIdx.x];
-    if (item < 0) return;
-    t = item_of(p, item);
-    n_rows = t.rows;
-  }
+  const long long n_rows = static_cast<long long>(p.Hkv) * p.B * p.R;
+  const long long row0 = static_cast<long long>(blockIdx.x) * kJoinRows, stride = static_cast<long long>(gridDim.x) * kJoinRows;
   for (long long base = row0; base < n_rows; base += stride) {
     const long long id = base + slot;
     bool live = id < n_rows;
@@ -1353,22 +1450,15 @@ __global__ void __launch_bounds__(kJoinThreads) prefix_join_kernel(const __grid_
     PartList l0, l1;
     l0.n = l1.n = 0;
     if (live) {
-      if (p.shared) {
-        const int per = p.B * p.R;
-        kvh = static_cast<int>(id / per);
-        const int rg = static_cast<int>(id - static_cast<long long>(kvh) * per);
-        b = p.div_r.div(rg, &rr);
-        if (p.n_prefix > 0) {
-          const int rt = rg / kRows;
-          l0 = parts_of(p, kvh * p.n_rt + rt, rg - rt * kRows, ctas);
-        }
-        if (p.tail_pages != nullptr) l1 = parts_of(p, p.n_prefix + b * p.Hkv + kvh, rr, ctas);
-      } else {
-        b = t.b;
-        kvh = t.kvh;
-        rr = t.row0 + static_cast<int>(id);
-        l0 = parts_of(p, item, static_cast<int>(id), ctas);
+      const int per = p.B * p.R;
+      kvh = static_cast<int>(id / per);
+      const int rg = static_cast<int>(id - static_cast<long long>(kvh) * per);
+      b = p.div_r.div(rg, &rr);
+      if (p.n_prefix > 0) {
+        const int rt = rg / kRows;
+        l0 = parts_of(p, kvh * p.n_rt + rt, rg - rt * kRows, ctas);
       }
+      if (p.tail_pages != nullptr) l1 = parts_of(p, p.n_prefix + b * p.Hkv + kvh, rr, ctas);
       s = p.div_g.div(rr, &gh);
       live = s < queries_of(p, b);
     }
@@ -1503,10 +1593,9 @@ Plan make_plan(long long B, long long Hkv, long long G, long long Sq, int D) {
     a.prefix_rows = 2LL * kMaxCtas * kRows;
     a.tail_rows = 0;
   }
-  const long long split = a.shared ? a.n_items : kMaxCtas;
   a.off_first = kStatusBytes + 2048 + 1024;
-  a.off_last = a.off_first + align_up(split * 4, 256);
-  a.off_l = a.off_last + align_up(split * 4, 256);
+  a.off_last = a.off_first + align_up(a.n_items * 4, 256);
+  a.off_l = a.off_last + align_up(a.n_items * 4, 256);
   const long long rows = a.prefix_rows + a.tail_rows + a.few_rows;
   a.off_acc = a.off_l + align_up(rows * 4, 256);
   a.bytes = a.off_acc + static_cast<size_t>(rows) * D * 4;
@@ -1599,9 +1688,10 @@ nabla_status launch(const AttnParams& p, const nabla_cache& cache, uint32_t* sta
   if (rc != NABLA_OK) return rc;
   const int ctas = sms < kMaxCtas ? sms : kMaxCtas, few_ctas = 2 * ctas;
   AttnParams a = p;
-  // Whole rounds keep the CTAs on few key heads at a time, which read the same key tiles at
-  // about the same time (uneven prompts: 340 us; all items cut into runs: 385 us).
-  a.whole = a.shared ? 0 : a.n_items / ctas;
+  // Whole rounds keep the CTAs on few key heads at a time (the L2 cache holds their keys);
+  // items of different lengths would make a round as long as its longest (uneven prompts:
+  // 327 us in rounds, 261 in runs).
+  a.whole = a.shared || a.uniform == 0 ? 0 : a.n_items / ctas;
   CUtensorMap mk, mv;
   if (a.few0 > 0 && (!make_map_pool(&mk, cache.k, cache) || !make_map_pool(&mv, cache.v, cache))) return NABLA_ERR_CUDA;
   cudaError_t e;
@@ -1615,12 +1705,14 @@ nabla_status launch(const AttnParams& p, const nabla_cache& cache, uint32_t* sta
     e = launch_behind(a.few1 > a.few0, prefix_attn_kernel<D, F16>, dim3(ctas), kThreads, C::kSmemBytes, st, mk, mv, a);
     if (e != cudaSuccess) return cuda_status(e);
   }
-  dim3 grid(ctas, kJoinBlocks);
   if (a.shared) {
     const long long blocks = (static_cast<long long>(a.Hkv) * a.B * a.R + kJoinRows - 1) / kJoinRows;
-    grid = dim3(static_cast<unsigned>(blocks < 1 << 20 ? blocks : 1 << 20));
+    e = launch_behind(true, prefix_join_kernel<D, F16>, dim3(static_cast<unsigned>(blocks < 1 << 20 ? blocks : 1 << 20)),
+                      kJoinThreads, 0, st, a, status, ctas, few_ctas);
+  } else {
+    e = launch_behind(true, own_join_kernel<D, F16>, dim3(ctas, kOwnJoinBlocks), kJoinThreads, 0, st, a, status, ctas);
   }
-  return cuda_status(launch_behind(true, prefix_join_kernel<D, F16>, grid, kJoinThreads, 0, st, a, status, ctas, few_ctas));
+  return cuda_status(e);
 }
 
 }  // namespace

@@ -80,8 +80,9 @@ class Problem:
 
     def run(self, **kw):
         m = nbl()
-        ws = torch.full((m.nabla_prefix_workspace_bytes(self.B, self.Hq, self.Hkv, self.Sq, self.D),), 0x5A,
-                        dtype=torch.uint8, device=DEV)
+        need = m.nabla_prefix_workspace_bytes(self.B, self.Hq, self.Hkv, self.Sq, self.D)
+        room = torch.full((need + 4096,), 0x5A, dtype=torch.uint8, device=DEV)
+        ws = room[:need]
         lse = torch.full((self.B, self.Hq, self.Sq), 77.0, dtype=F32, device=DEV)
         o = torch.full((self.B, self.Hq, self.Sq, self.D), 55.0, dtype=kw.pop("o_dtype", self.dtype), device=DEV)
         a = {**self.args(), "o": o, "lse": lse, "workspace": ws, **kw}
@@ -89,6 +90,7 @@ class Problem:
         m.nabla_prefix_attn(q, *self.caches, **a)
         torch.cuda.synchronize()
         assert m.nabla_read_device_status(ws) == 0
+        assert (room[need:] == 0x5A).all()
         return a["o"], a["lse"]
 
     def oracle(self, absolute=False):
@@ -159,6 +161,11 @@ CASES = {
     "chunk part f16": dict(B=1, Hq=2, Hkv=2, D=64, Sq=300, P=513, tails=None, page=256, part=F16, dtype=F16),
     # more items than CTAs: whole rounds, then a split remainder
     "rounds": dict(B=2, Hq=40, Hkv=40, D=128, Sq=513, P=300, tails=None, page=64),
+    "many sequences": dict(B=300, Hq=2, Hkv=2, D=64, Sq=1, P=40, tails=[(7 * i) % 50 for i in range(300)], page=16),
+    "group of 16": dict(B=2, Hq=32, Hkv=2, D=128, Sq=1, P=333, tails=[129, 1], page=32, dtype=F16),
+    "group of 17": dict(B=2, Hq=17, Hkv=1, D=64, Sq=1, P=333, tails=[129, 0], page=32),
+    "uneven items": dict(B=4, Hq=40, Hkv=40, D=64, Sq=300, P=130, tails=[300, 7, 0, 290], page=64,
+                         q_len=[300, 7, 0, 260]),
     "rounds causal": dict(B=3, Hq=18, Hkv=9, D=64, Sq=700, P=60, tails=[700, 350, 720], page=16, causal=True,
                           q_len=[700, 300, 650], part=BF),
 }

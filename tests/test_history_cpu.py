@@ -152,5 +152,88 @@ def test_binding_refuses(nb):
         nb.Rope(freq.float())
     with pytest.raises(ValueError):
         nb.Rope.build(64, "cpu", axis_dims=(20, 20, 20))
+    rope = nb.Rope(freq)
+    with pytest.raises(ValueError, match="CUDA"):
+        nb.nabla_rotary(x, None, rope)
     with pytest.raises(ValueError):
-        nb.nabla_rotary(x, None, nb.Rope(freq))                        # not on a GPU
+        nb.nabla_rotary(None, None, rope)
+    with pytest.raises(TypeError):
+        nb.nabla_rotary([1.0], None, rope)
+    with pytest.raises(ValueError, match="CUDA"):
+        nb.nabla_cache_append(x, x, x, x, freq, freq)
+    with pytest.raises(ValueError, match="CUDA"):
+        nb.nabla_prefix_attn(x, x, x, None, 0)
+
+
+def test_oracle_prefix_attention():
+    """Against torch's attention over gathered keys, a merge against the union, and empty rows."""
+    rng = np.random.default_rng(3)
+    B, Hq, Hkv, Sq, D, page, P, tails = 2, 4, 2, 3, 64, 16, 21, [5, 17]
+    kc, vc = rng.normal(size=(2, 8, Hkv, page, D))
+    q = rng.normal(size=(B, Hq, Sq, D))
+    prefix, table = [6, 1], [[0, 2], [4, 5]]
+    for causal in (False, True):
+        o, lse = H.prefix_attention(q, kc, vc, prefix, P, table, tails, [Sq] * B, causal, 0.125)
+        for b in range(B):
+            pages = [(prefix[j // page], j % page) for j in range(P)] + [(table[b][j // page], j % page) for j in range(tails[b])]
+            k = np.stack([kc[p, :, s] for p, s in pages], 1).repeat(Hq // Hkv, 0)
+            v = np.stack([vc[p, :, s] for p, s in pages], 1).repeat(Hq // Hkv, 0)
+            n = len(pages)
+            mask = torch.ones(Sq, n, dtype=torch.bool).tril(n - Sq) if causal else None
+            ref = torch.nn.functional.scaled_dot_product_attention(
+                torch.tensor(q[b]), torch.tensor(k), torch.tensor(v), attn_mask=mask, scale=0.125)
+            np.testing.assert_allclose(o[b], ref.numpy(), atol=1e-12)
+    # prefix alone merged with tails alone = both
+    both, bl = H.prefix_attention(q, kc, vc, prefix, P, table, tails, [Sq] * B, False, 0.125)
+    po, pl = H.prefix_attention(q, kc, vc, [], 0, table, tails, [Sq] * B, False, 0.125)
+    o, lse = H.prefix_attention(q, kc, vc, prefix, P, table, [0, 0], [Sq] * B, False, 0.125, po, pl)
+    np.testing.assert_allclose(o, both, atol=1e-12)
+    np.testing.assert_allclose(lse, bl, atol=1e-12)
+    o, lse = H.prefix_attention(q, kc, vc, [], 0, table, [1, 0], [3, 2], True, 0.125)
+    assert np.isneginf(lse[0, :, :2]).all() and (o[0, :, :2] == 0).all() and np.isfinite(lse[0, :, 2]).all()
+    assert np.isneginf(lse[1, :, :2]).all() and np.isnan(o[1, :, 2]).all()
+
+
+def test_prefix_attn_refuses(nb):
+    lib = nb.load_library()
+    INV, UNS, WS = nb.NABLA_ERR_INVALID_ARG, nb.NABLA_ERR_UNSUPPORTED, nb.NABLA_ERR_WORKSPACE
+    need = lib.nabla_prefix_workspace_bytes(1, 4, 2, 32, 64)
+    assert need > 256
+    for bad in ((0, 4, 2, 32, 64), (1, 3, 2, 32, 64), (1, 4, 0, 32, 64), (1, 4, 2, 0, 64), (1, 4, 2, 32, 96),
+                (1 << 20, 4, 2, 1 << 20, 64)):
+        assert lib.nabla_prefix_workspace_bytes(*bad) == 0
+    Q, K, V, O, L, W = (0x10000000 * i for i in range(1, 7))
+
+    def call(q=None, B=1, Sq=32, cache=None, pages=0x1000, P=20, tail=0x2000, width=4, tlen=0x3000, qlen=None, causal=0,
+             scale=0.125, part=nb._Heads(), plse=None, o=None, lse=L, ws=W, wsb=need):
+        return lib.nabla_prefix_attn(q or _view(nb, Q, Hh=4), B, Sq, cache or nb._Cache(K, V, 4, 2, 16, 64, 0), pages,
+                                     P, tail, width, tlen, qlen, causal, scale, part, plse,
+                                     o or _view(nb, O, Hh=4), lse, ws, wsb, None)
+    # sizes, dtypes, views
+    assert call(B=0) == INV and call(Sq=0) == INV
+    assert call(q=_view(nb, Q, Hh=3), o=_view(nb, O, Hh=3)) == INV          # 3 heads on 2 key heads
+    assert call(q=_view(nb, Q, Hh=4, dtype=2)) == INV                        # fp16 on a bf16 cache
+    assert call(o=_view(nb, O, Hh=2)) == INV and call(o=_view(nb, O, Hh=4, dtype=2)) == INV
+    assert call(q=_view(nb, Q + 8, Hh=4)) == INV and call(o=_view(nb, O, Hh=4, stride_s=0)) == INV
+    assert call(cache=nb._Cache(K, V, 4, 2, 48, 64, 0)) == UNS and call(cache=nb._Cache(K, V, 4, 2, 16, 32, 0)) == UNS
+    assert call(cache=nb._Cache(K, V, 4, 2, 16, 64, 1)) == INV and call(cache=nb._Cache(None, V, 4, 2, 16, 64, 0)) == INV
+    # prefix and tails
+    assert call(P=-1) == INV and call(pages=None) == INV and call(pages=0x1002) == INV
+    assert call(tlen=None) == INV and call(width=0) == INV and call(tail=None) == INV
+    assert call(qlen=0x3001) == INV and call(causal=2) == INV
+    assert call(P=2147483647) == UNS and call(width=1 << 28) == UNS
+    for scale in (0.0, -1.0, math.nan, math.inf):
+        assert call(scale=scale) == INV
+    # the merged part
+    part = _view(nb, 0x70000000, Hh=4, dtype=1)
+    assert call(part=part) == INV and call(plse=0x71000000) == INV           # one without the other
+    assert call(part=_view(nb, 0x70000000, Hh=4, dtype=2), plse=0x71000000) == INV
+    assert call(part=_view(nb, 0x70000000, Hh=2, dtype=1), plse=0x71000000) == INV
+    assert call(part=_view(nb, O, Hh=4, dtype=1), plse=0x71000000) == INV    # over o, but not o itself
+    assert call(part=part, plse=O) == INV and call(part=part, plse=L + 4) == INV
+    # outputs over inputs
+    assert call(o=_view(nb, Q, Hh=4)) == INV and call(o=_view(nb, K, Hh=4)) == INV
+    assert call(lse=O) == INV and call(lse=Q) == INV and call(lse=V) == INV
+    assert call(lse=L + 2) == INV
+    # workspace
+    assert call(ws=None) == WS and call(wsb=need - 1) == WS and call(ws=W + 16) == WS
