@@ -15,10 +15,13 @@
 // of several heads in flight.  Neighbouring threads own a token's neighbouring pairs and
 // then the neighbouring tokens, so a head's accesses are contiguous runs.
 //
-// Half-split pairs (i, i + dim / 2) with dim / 2 not a multiple of 8 have no common
-// 16-byte alignment of the two parts.  Then a thread owns 8 consecutive output elements
-// and reads their partners one by one from the row its neighbours load (L1 hits).
+// Half-split pairs (i, i + dim / 2) with dim / 2 no multiple of 8 have no common 16-byte
+// alignment of their parts: rotary_staged_kernel turns them in shared memory (97 MB of f32
+// rows with 38 pairs: 26 us; 38.5 us with partners read one by one from L1; vectors that
+// divide dim / 2 ran at 1 TB/s where it is odd).
 #include <math.h>
+
+#include <type_traits>
 
 #include "history.cuh"
 
@@ -26,7 +29,7 @@ namespace nabla {
 namespace {
 
 constexpr int kThreads = 128;
-enum { kInterleaved = 0, kHalf = 1, kHalfOdd = 2 };   // pairing; kHalfOdd: dim / 2 % 8 != 0
+enum { kInterleaved = 0, kHalf = 1 };   // pairing
 
 // One tensor to move: source and destination views (strides in elements).
 struct Stream {
@@ -60,81 +63,58 @@ struct RotaryParams {
   uint32_t* status;
 };
 
-template <typename T>
-struct Row8;   // 8 consecutive elements
-template <>
-struct Row8<__nv_bfloat16> {
-  uint4 v;
-  __device__ __forceinline__ void load(const __nv_bfloat16* p) { v = __ldg(reinterpret_cast<const uint4*>(p)); }
-  __device__ __forceinline__ void store(__nv_bfloat16* p) const { *reinterpret_cast<uint4*>(p) = v; }
-  __device__ __forceinline__ void get(float (&f)[8]) const {
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+__device__ __forceinline__ float to_float(__nv_bfloat16 x) { return __bfloat162float(x); }
+__device__ __forceinline__ float to_float(__half x) { return __half2float(x); }
+__device__ __forceinline__ float to_float(float x) { return x; }
+
+// V consecutive elements, whole 16-byte words.
+template <typename T, int V>
+struct Vec {
+  using W = uint4;
+  static constexpr int kWords = V * sizeof(T) / 16;
+  union {
+    W w[kWords];
+    T e[V];
+  };
+  __device__ __forceinline__ Vec() {}
+  __device__ __forceinline__ void load(const T* p) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      f[2 * i] = __uint_as_float(w[i] << 16);
-      f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-    }
+    for (int i = 0; i < kWords; ++i) w[i] = __ldg(reinterpret_cast<const W*>(p) + i);
   }
-  __device__ __forceinline__ void set(const float (&f)[8]) {
-    v = make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
-  }
-};
-template <>
-struct Row8<__half> {
-  uint4 v;
-  __device__ __forceinline__ void load(const __half* p) { v = __ldg(reinterpret_cast<const uint4*>(p)); }
-  __device__ __forceinline__ void store(__half* p) const { *reinterpret_cast<uint4*>(p) = v; }
-  __device__ __forceinline__ void get(float (&f)[8]) const {
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  __device__ __forceinline__ void store(T* p) const {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
-      f[2 * i] = x.x;
-      f[2 * i + 1] = x.y;
+    for (int i = 0; i < kWords; ++i) reinterpret_cast<W*>(p)[i] = w[i];
+  }
+  __device__ __forceinline__ void get(float (&f)[V]) const {
+#pragma unroll
+    for (int i = 0; i < V; ++i) f[i] = to_float(e[i]);
+  }
+  __device__ __forceinline__ void set(const float (&f)[V]) {
+    if constexpr (sizeof(T) == 2) {
+#pragma unroll
+      for (int i = 0; i < V; i += 2)
+        reinterpret_cast<uint32_t*>(w)[i / 2] =
+            std::is_same<T, __half>::value ? pack_f16x2(f[i], f[i + 1]) : pack_bf16x2(f[i], f[i + 1]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < V; ++i) e[i] = f[i];
     }
-  }
-  __device__ __forceinline__ void set(const float (&f)[8]) {
-    v = make_uint4(pack_f16x2(f[0], f[1]), pack_f16x2(f[2], f[3]), pack_f16x2(f[4], f[5]), pack_f16x2(f[6], f[7]));
-  }
-};
-template <>
-struct Row8<float> {
-  float4 a, b;
-  __device__ __forceinline__ void load(const float* p) {
-    a = __ldg(reinterpret_cast<const float4*>(p));
-    b = __ldg(reinterpret_cast<const float4*>(p) + 1);
-  }
-  __device__ __forceinline__ void store(float* p) const {
-    reinterpret_cast<float4*>(p)[0] = a;
-    reinterpret_cast<float4*>(p)[1] = b;
-  }
-  __device__ __forceinline__ void get(float (&f)[8]) const {
-    f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
-    f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
-  }
-  __device__ __forceinline__ void set(const float (&f)[8]) {
-    a = make_float4(f[0], f[1], f[2], f[3]);
-    b = make_float4(f[4], f[5], f[6], f[7]);
   }
 };
 
 // The same elements in another type (a plain copy when the types agree).
-template <typename TD, typename TS>
-__device__ __forceinline__ Row8<TD> convert(const Row8<TS>& x) {
-  if constexpr (sizeof(TD) == sizeof(TS)) {
-    return *reinterpret_cast<const Row8<TD>*>(&x);   // only instantiated for equal types
+template <typename TD, typename TS, int V>
+__device__ __forceinline__ Vec<TD, V> convert(const Vec<TS, V>& x) {
+  if constexpr (std::is_same<TD, TS>::value) {
+    return x;
   } else {
-    float f[8];
+    float f[V];
     x.get(f);
-    Row8<TD> y;
+    Vec<TD, V> y;
     y.set(f);
     return y;
   }
 }
-
-__device__ __forceinline__ float to_float(__nv_bfloat16 x) { return __bfloat162float(x); }
-__device__ __forceinline__ float to_float(__half x) { return __half2float(x); }
-__device__ __forceinline__ float to_float(float x) { return x; }
 
 // What a thread knows about its token.
 struct Token {
@@ -216,8 +196,9 @@ __device__ __forceinline__ void angle(const RotaryParams& p, const Token& k, int
 
 template <int PAIRING, int D, typename TS, typename TD>
 __global__ void __launch_bounds__(kThreads) rotary_kernel(const __grid_constant__ RotaryParams p) {
-  constexpr int kLanes = PAIRING == kHalfOdd ? D / 8 : D / 16;          // threads per token
-  constexpr int kUnroll = 2;
+  constexpr int V = 8;
+  constexpr int kLanes = D / (2 * V);                      // threads per token
+  constexpr int kUnroll = 2;                               // heads in flight
   const long long gid = static_cast<long long>(blockIdx.x) * kThreads + threadIdx.x;
   const long long token = gid / kLanes;
   if (token >= p.tokens) return;
@@ -228,34 +209,33 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(const __grid_constant_
 
   // Element offsets of the thread's two vectors, and its pairs' factors.  A pair that is
   // not rotated is copied, not multiplied by one: its values may be infinite.
-  int e0, e1 = 0;
-  bool turn[8];
-  float c[8], s[8];
-  if constexpr (PAIRING == kHalfOdd) {
-    e0 = 8 * u;
-  } else if constexpr (PAIRING == kHalf) {
-    const bool rot = 8 * u < p.half;
-    e0 = rot ? 8 * u : 2 * p.half + (8 * u - p.half) * 2;
-    e1 = rot ? p.half + 8 * u : e0 + 8;
+  int e0, e1;
+  bool turn[V];
+  float c[V], s[V];
+  if constexpr (PAIRING == kHalf) {
+    const bool rot = V * u < p.half;
+    e0 = rot ? V * u : 2 * p.half + (V * u - p.half) * 2;
+    e1 = rot ? p.half + V * u : e0 + V;
   } else {
-    e0 = 16 * u;
-    e1 = e0 + 8;
+    e0 = 2 * V * u;
+    e1 = e0 + V;
   }
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    int i = 8 * u + j;
-    turn[j] = i < p.half;
-    if constexpr (PAIRING == kHalfOdd) {
-      turn[j] = i < 2 * p.half;
-      if (i >= p.half) i -= p.half;
-    }
+  for (int j = 0; j < V; ++j) {
+    turn[j] = V * u + j < p.half;
     c[j] = 1.f;
     s[j] = 0.f;
-    if (turn[j]) angle(p, k, i, &c[j], &s[j]);
+    if (turn[j]) angle(p, k, V * u + j, &c[j], &s[j]);
   }
 
   // A head of the list -> its stream, whether it is rotated and whether it is written.
   auto stream_of = [&](int h) { return h < p.st[0].end ? 0 : (h < p.st[1].end ? 1 : 2); };
+  auto source = [&](int i, int hh) {
+    return static_cast<const TS*>(p.st[i].src) + (i == 0 ? k.src[0] : (i == 1 ? k.src[1] : k.src[2])) + hh * p.st[i].s_h;
+  };
+  auto target = [&](int i, int hh) {
+    return static_cast<TD*>(p.st[i].dst) + (i == 0 ? k.dst[0] : (i == 1 ? k.dst[1] : k.dst[2])) + hh * p.st[i].d_h;
+  };
   for (int h0 = h_begin; h0 < h_end; h0 += kUnroll) {
     const TS* src[kUnroll];
     TD* dst[kUnroll];
@@ -267,94 +247,142 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(const __grid_constant_
       const int hh = h - (i == 0 ? 0 : p.st[i - 1].end);
       go[x] = h < h_end && (i == 0 || k.stored);
       rot[x] = i < 2;
-      src[x] = static_cast<const TS*>(p.st[i].src) + (i == 0 ? k.src[0] : (i == 1 ? k.src[1] : k.src[2])) + hh * p.st[i].s_h;
-      dst[x] = static_cast<TD*>(p.st[i].dst) + (i == 0 ? k.dst[0] : (i == 1 ? k.dst[1] : k.dst[2])) + hh * p.st[i].d_h;
+      src[x] = source(i, hh);
+      dst[x] = target(i, hh);
     }
-    if constexpr (PAIRING == kHalfOdd) {
+    Vec<TS, V> a[kUnroll], b[kUnroll];
 #pragma unroll
-      for (int x = 0; x < kUnroll; ++x) {
-        if (!go[x]) continue;
-        Row8<TS> a;
-        a.load(src[x] + e0);
-        if (!rot[x]) {
-          convert<TD>(a).store(dst[x] + e0);
-          continue;
-        }
-        float f[8], o[8];
-        a.get(f);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const int e = e0 + j;
-          o[j] = f[j];
-          if (turn[j]) {
-            const bool low = e < p.half;
-            const float g = to_float(src[x][low ? e + p.half : e - p.half]);
-            o[j] = low ? f[j] * c[j] - g * s[j] : f[j] * c[j] + g * s[j];
-          }
-        }
-        Row8<TD> y;
-        y.set(o);
-        y.store(dst[x] + e0);
+    for (int x = 0; x < kUnroll; ++x) {
+      if (go[x]) {
+        a[x].load(src[x] + e0);
+        b[x].load(src[x] + e1);
       }
-    } else {
-      Row8<TS> a[kUnroll], b[kUnroll];
+    }
 #pragma unroll
-      for (int x = 0; x < kUnroll; ++x) {
-        if (go[x]) {
-          a[x].load(src[x] + e0);
-          b[x].load(src[x] + e1);
-        }
-      }
+    for (int x = 0; x < kUnroll; ++x) {
+      if (!go[x]) continue;
+      Vec<TD, V> ya, yb;
+      if (rot[x]) {
+        float f[V], g[V];
+        a[x].get(f);
+        b[x].get(g);
+        if constexpr (PAIRING == kHalf) {
 #pragma unroll
-      for (int x = 0; x < kUnroll; ++x) {
-        if (!go[x]) continue;
-        Row8<TD> ya, yb;
-        if (rot[x]) {
-          float f[8], g[8];
-          a[x].get(f);
-          b[x].get(g);
-          if constexpr (PAIRING == kHalf) {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              if (turn[j]) {
-                const float x0 = f[j], x1 = g[j];
-                f[j] = x0 * c[j] - x1 * s[j];
-                g[j] = x1 * c[j] + x0 * s[j];
-              }
-            }
-          } else {
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              if (turn[j]) {
-                const float x0 = f[2 * j], x1 = f[2 * j + 1];
-                f[2 * j] = x0 * c[j] - x1 * s[j];
-                f[2 * j + 1] = x1 * c[j] + x0 * s[j];
-              }
-              if (turn[4 + j]) {
-                const float x0 = g[2 * j], x1 = g[2 * j + 1];
-                g[2 * j] = x0 * c[4 + j] - x1 * s[4 + j];
-                g[2 * j + 1] = x1 * c[4 + j] + x0 * s[4 + j];
-              }
+          for (int j = 0; j < V; ++j) {
+            if (turn[j]) {
+              const float x0 = f[j], x1 = g[j];
+              f[j] = x0 * c[j] - x1 * s[j];
+              g[j] = x1 * c[j] + x0 * s[j];
             }
           }
-          ya.set(f);
-          yb.set(g);
         } else {
-          ya = convert<TD>(a[x]);
-          yb = convert<TD>(b[x]);
+#pragma unroll
+          for (int j = 0; j < V / 2; ++j) {
+            if (turn[j]) {
+              const float x0 = f[2 * j], x1 = f[2 * j + 1];
+              f[2 * j] = x0 * c[j] - x1 * s[j];
+              f[2 * j + 1] = x1 * c[j] + x0 * s[j];
+            }
+            if (turn[V / 2 + j]) {
+              const float x0 = g[2 * j], x1 = g[2 * j + 1];
+              g[2 * j] = x0 * c[V / 2 + j] - x1 * s[V / 2 + j];
+              g[2 * j + 1] = x1 * c[V / 2 + j] + x0 * s[V / 2 + j];
+            }
+          }
         }
-        ya.store(dst[x] + e0);
-        yb.store(dst[x] + e1);
+        ya.set(f);
+        yb.set(g);
+      } else {
+        ya = convert<TD>(a[x]);
+        yb = convert<TD>(b[x]);
+      }
+      ya.store(dst[x] + e0);
+      yb.store(dst[x] + e1);
+    }
+  }
+}
+
+// Any dim / 2.  A warp owns a token and a run of heads, eight at a time: rows come in
+// 16-byte vectors, are widened into shared memory, turned there (a lane has pairs lane and
+// lane + 32) and leave in 16-byte vectors.  (Eight tokens of one head at a time, with their
+// angles in shared memory, was slower: 186 against 145 us on 588 MB.)
+constexpr int kStagedRows = 8, kStagedWarps = 8;
+template <int D, typename TS, typename TD>
+__global__ void __launch_bounds__(kThreads) rotary_staged_kernel(const __grid_constant__ RotaryParams p) {
+  constexpr int kVs = 16 / sizeof(TS), kVd = 16 / sizeof(TD);            // elements of a vector
+  constexpr int kLoads = kStagedRows * D / (kVs * 32), kStores = kStagedRows * D / (kVd * 32);
+  constexpr int kPairs = D / 64;                                         // pairs of a lane
+  __shared__ __align__(16) float rows[kThreads / 32][kStagedRows][D];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const long long token = static_cast<long long>(blockIdx.x) * (kThreads / 32) + warp;
+  if (token >= p.tokens) return;                                         // whole warps
+  const Token k = locate(p, static_cast<int>(token));
+  const int h_begin = blockIdx.y * p.group;
+  const int h_end = min(h_begin + p.group, p.heads);
+  float c[kPairs], s[kPairs];
+#pragma unroll
+  for (int j = 0; j < kPairs; ++j)
+    if (lane + 32 * j < p.half) angle(p, k, lane + 32 * j, &c[j], &s[j]);
+  float(*row)[D] = rows[warp];
+  auto written = [&](int h) { return h < h_end && (h < p.st[0].end || k.stored); };
+  for (int h0 = h_begin; h0 < h_end; h0 += kStagedRows) {
+    Vec<TS, kVs> a[kLoads];
+#pragma unroll
+    for (int n = 0; n < kLoads; ++n) {
+      const int f = n * 32 + lane, h = h0 + f / (D / kVs), e = f % (D / kVs) * kVs;
+      const int i = h < p.st[0].end ? 0 : (h < p.st[1].end ? 1 : 2);
+      if (written(h))
+        a[n].load(static_cast<const TS*>(p.st[i].src) + (i == 0 ? k.src[0] : (i == 1 ? k.src[1] : k.src[2])) +
+                  (h - (i == 0 ? 0 : p.st[i - 1].end)) * p.st[i].s_h + e);
+    }
+#pragma unroll
+    for (int n = 0; n < kLoads; ++n) {
+      const int f = n * 32 + lane, r = f / (D / kVs), e = f % (D / kVs) * kVs;
+      if (!written(h0 + r)) continue;
+      float x[kVs];
+      a[n].get(x);
+#pragma unroll
+      for (int v = 0; v < kVs; v += 4) *reinterpret_cast<float4*>(&row[r][e + v]) = make_float4(x[v], x[v + 1], x[v + 2], x[v + 3]);
+    }
+    __syncwarp();
+    const int turned = min(min(h_end, p.st[1].end) - h0, kStagedRows);
+    for (int r = 0; r < turned; ++r) {
+#pragma unroll
+      for (int j = 0; j < kPairs; ++j) {
+        const int i = lane + 32 * j;
+        if (i < p.half) {
+          const float x0 = row[r][i], x1 = row[r][i + p.half];
+          row[r][i] = x0 * c[j] - x1 * s[j];
+          row[r][i + p.half] = x1 * c[j] + x0 * s[j];
+        }
       }
     }
+    __syncwarp();
+#pragma unroll
+    for (int n = 0; n < kStores; ++n) {
+      const int f = n * 32 + lane, r = f / (D / kVd), h = h0 + r, e = f % (D / kVd) * kVd;
+      const int i = h < p.st[0].end ? 0 : (h < p.st[1].end ? 1 : 2);
+      if (!written(h)) continue;
+      float x[kVd];
+#pragma unroll
+      for (int v = 0; v < kVd; v += 4) {
+        const float4 y = *reinterpret_cast<const float4*>(&row[r][e + v]);
+        x[v] = y.x; x[v + 1] = y.y; x[v + 2] = y.z; x[v + 3] = y.w;
+      }
+      Vec<TD, kVd> y;
+      y.set(x);
+      y.store(static_cast<TD*>(p.st[i].dst) + (i == 0 ? k.dst[0] : (i == 1 ? k.dst[1] : k.dst[2])) +
+              (h - (i == 0 ? 0 : p.st[i - 1].end)) * p.st[i].d_h + e);
+    }
+    __syncwarp();
   }
 }
 
 template <int PAIRING, int D, typename TS, typename TD>
 cudaError_t go(RotaryParams p, cudaStream_t st) {
-  constexpr int kLanes = PAIRING == kHalfOdd ? D / 8 : D / 16;
+  constexpr int kLanes = D / 16;
   const long long lanes = static_cast<long long>(p.tokens) * kLanes;
-  // Heads per thread: as many as leave about 5 warps of threads on each of the GPU's 592
+  // Heads per thread: as many as leave about 6 warps of threads on each of the GPU's 592
   // schedulers, so that the angles (about 3 us of latency) are shared by many heads; a small
   // call spreads its heads over threads instead.  Sequences [3, 4097] of 24 heads: 118 us at
   // one head a thread, 33 us at four and more; blocks of 128 threads and two heads in flight
@@ -368,25 +396,38 @@ cudaError_t go(RotaryParams p, cudaStream_t st) {
   return cudaGetLastError();
 }
 
+template <int D, typename TS, typename TD>
+cudaError_t go_staged(RotaryParams p, cudaStream_t st) {
+  // heads per warp: as many as leave about 8 warps on each scheduler
+  long long g = static_cast<long long>(p.tokens) * p.heads / (592LL * kStagedWarps);
+  if (g > kStagedRows) g = (g + kStagedRows - 1) / kStagedRows * kStagedRows;
+  g = g < 1 ? 1 : (g > p.heads ? p.heads : g);
+  p.group = static_cast<int>(g);
+  constexpr int kWarps = kThreads / 32;
+  dim3 grid(static_cast<unsigned>((static_cast<long long>(p.tokens) + kWarps - 1) / kWarps),
+            static_cast<unsigned>((p.heads + g - 1) / g));
+  rotary_staged_kernel<D, TS, TD><<<grid, kThreads, 0, st>>>(p);
+  return cudaGetLastError();
+}
+
+template <int D, typename TS, typename TD>
+cudaError_t by_pairing(const RotaryParams& p, int style, cudaStream_t st) {
+  if (style == NABLA_ROPE_INTERLEAVED) return go<kInterleaved, D, TS, TD>(p, st);
+  return p.half % 8 == 0 ? go<kHalf, D, TS, TD>(p, st) : go_staged<D, TS, TD>(p, st);
+}
+
 template <typename TS, typename TD>
-cudaError_t by_pairing(const RotaryParams& p, int style, int D, cudaStream_t st) {
-  const int pairing = style == NABLA_ROPE_INTERLEAVED ? kInterleaved : (p.half % 8 ? kHalfOdd : kHalf);
-  if (D == 64)
-    return pairing == kInterleaved ? go<kInterleaved, 64, TS, TD>(p, st)
-           : pairing == kHalf      ? go<kHalf, 64, TS, TD>(p, st)
-                                   : go<kHalfOdd, 64, TS, TD>(p, st);
-  return pairing == kInterleaved ? go<kInterleaved, 128, TS, TD>(p, st)
-         : pairing == kHalf      ? go<kHalf, 128, TS, TD>(p, st)
-                                 : go<kHalfOdd, 128, TS, TD>(p, st);
+cudaError_t by_width(const RotaryParams& p, int style, int D, cudaStream_t st) {
+  return D == 64 ? by_pairing<64, TS, TD>(p, style, st) : by_pairing<128, TS, TD>(p, style, st);
 }
 
 cudaError_t by_dtype(const RotaryParams& p, int style, int D, int src, int dst, cudaStream_t st) {
   using bf = __nv_bfloat16;
-  if (src == NABLA_BF16) return dst == NABLA_BF16 ? by_pairing<bf, bf>(p, style, D, st) : by_pairing<bf, float>(p, style, D, st);
-  if (src == NABLA_F16) return dst == NABLA_F16 ? by_pairing<__half, __half>(p, style, D, st) : by_pairing<__half, float>(p, style, D, st);
-  return dst == NABLA_F32    ? by_pairing<float, float>(p, style, D, st)
-         : dst == NABLA_BF16 ? by_pairing<float, bf>(p, style, D, st)
-                             : by_pairing<float, __half>(p, style, D, st);
+  if (src == NABLA_BF16) return dst == NABLA_BF16 ? by_width<bf, bf>(p, style, D, st) : by_width<bf, float>(p, style, D, st);
+  if (src == NABLA_F16) return dst == NABLA_F16 ? by_width<__half, __half>(p, style, D, st) : by_width<__half, float>(p, style, D, st);
+  return dst == NABLA_F32    ? by_width<float, float>(p, style, D, st)
+         : dst == NABLA_BF16 ? by_width<float, bf>(p, style, D, st)
+                             : by_width<float, __half>(p, style, D, st);
 }
 
 nabla_status check_rope(const nabla_rope& r, int D) {

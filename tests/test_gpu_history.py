@@ -54,6 +54,10 @@ PLAIN = [
     (2, 65, 4, 2, 64, 62, True, torch.float32, torch.float16, False, False),
     (1, 77, 3, 1, 64, 64, False, torch.float32, torch.float32, True, False),
     (1, 4097, 2, 1, 128, 34, False, torch.float16, torch.float16, False, True),
+    (2, 70, 3, 2, 128, 76, False, torch.float32, torch.bfloat16, True, False),
+    (2, 70, 13, 2, 128, 10, False, torch.bfloat16, torch.bfloat16, True, False),
+    (2, 70, 3, 12, 64, 50, False, torch.float16, torch.float16, True, True),
+    (2, 70, 3, 2, 64, 56, False, torch.bfloat16, torch.bfloat16, False, False),
     (1, 900, 40, 40, 128, 128, True, torch.bfloat16, torch.bfloat16, True, False),
 ]
 
@@ -185,6 +189,10 @@ APPEND = [
     (3, 77, 2, 6, 128, 126, False, 3, 32, torch.float16, True),
     (4, 300, 3, 3, 64, 18, True, 1, 16, torch.float16, True),
     (2, 200, 5, 0, 128, 128, True, 3, 256, torch.bfloat16, False),
+    (2, 40, 7, 5, 128, 6, False, 1, 16, torch.bfloat16, True),
+    (2, 40, 7, 0, 64, 62, False, 1, 16, torch.bfloat16, True),
+    (3, 33, 9, 2, 128, 108, False, 1, 32, torch.float16, True),
+    (2, 21, 5, 3, 64, 40, False, 1, 32, torch.float16, False),
     (5, 9, 1, 4, 64, 64, False, 1, 4096, torch.bfloat16, True),
 ]
 
