@@ -382,12 +382,13 @@ template <int PAIRING, int D, typename TS, typename TD>
 cudaError_t go(RotaryParams p, cudaStream_t st) {
   constexpr int kLanes = D / 16;
   const long long lanes = static_cast<long long>(p.tokens) * kLanes;
-  // Heads per thread: as many as leave about 6 warps of threads on each of the GPU's 592
+  // Heads per thread: as many as leave about 8 warps of threads on each of the GPU's 592
   // schedulers, so that the angles (about 3 us of latency) are shared by many heads; a small
   // call spreads its heads over threads instead.  Sequences [3, 4097] of 24 heads: 118 us at
-  // one head a thread, 33 us at four and more; blocks of 128 threads and two heads in flight
-  // beat 256 and four (720p-like Q and K 499 against 507 us).
-  long long g = lanes * p.heads / (148LL * 768);
+  // one head a thread, 33 us at four and more.  One sequence of 7,168 tokens, 48 heads: 37 us
+  // at 8 warps, 43 at 6 and at 4, 39 at 12.  Blocks of 128 threads and two heads in flight beat
+  // 256 and four (720p-like Q and K 499 against 507 us).
+  long long g = lanes * p.heads / (148LL * 1024);
   g = g < 1 ? 1 : (g > p.heads ? p.heads : g);
   const int groups = static_cast<int>((p.heads + g - 1) / g);
   p.group = (p.heads + groups - 1) / groups;
