@@ -326,6 +326,7 @@ PyObject* prefix_attn(PyObject*, PyObject* const* a, Py_ssize_t n) {
     }
     const float scale = a[9] == Py_None ? static_cast<float>(1.0 / std::sqrt(static_cast<double>(D))) : static_cast<float>(real(a[9]));
     const int causal = PyObject_IsTrue(a[8]);
+    if (causal < 0) throw python_error();
     const nabla_status rc = nabla_prefix_attn(
         qv, b32, s32, cache, prefix ? table(prefix, {prefix->size(0)}, "prefix_pages") : nullptr, prefix_len,
         tail ? table(tail, {B, tail->size(1)}, "tail_pages") : nullptr, tail ? dim32(*tail, 1, "tail_pages") : 0,

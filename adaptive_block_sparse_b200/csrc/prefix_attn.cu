@@ -326,7 +326,8 @@ __device__ __forceinline__ bool bar_wait(uint64_t* bar, uint32_t parity, uint32_
         record_status(status, code);
         return false;
       }
-      if (*reinterpret_cast<volatile uint32_t*>(status) != 0u) return false;
+      // another wait of the CTA gave up (a bad page or length ends none)
+      if (*reinterpret_cast<volatile uint32_t*>(status) >> 8 == kDevTimeoutTmaFull >> 8) return false;
     }
   }
   return true;
@@ -353,12 +354,12 @@ __device__ __forceinline__ long long part_row(const AttnParams& p, int i, int ct
 // 2^y for a pair of arguments, without the special-function unit: y = n + f with n
 // whole and |f| <= 1/2 (adding 1.5 * 2^23 leaves n in the low mantissa bits), 2^f by the
 // minimax polynomial of degree 4 (Remez exchange on [-1/2, 1/2], relative error below
-// 2.6e-6), and n added to the exponent.  Results end at 2^-126 and 2^127 (a NaN gives one
-// of them).
+// 2.6e-6), and n added to the exponent.  Results end at 2^-126 and 2^127; a NaN gives
+// 2^127, which no row's sum may hold, so its tile is done again without the polynomial.
 __device__ __forceinline__ float2 poly_exp2(float2 y) {
   const float2 magic = make_float2(12582912.f, 12582912.f), back = make_float2(-12582912.f, -12582912.f);
-  y.x = fminf(fmaxf(y.x, -126.f), 127.f);
-  y.y = fminf(fmaxf(y.y, -126.f), 127.f);
+  y.x = fmaxf(fminf(y.x, 127.f), -126.f);
+  y.y = fmaxf(fminf(y.y, 127.f), -126.f);
   const float2 t = __fadd2_rn(y, magic);
   const float2 n = __fadd2_rn(t, back);
   const float2 f = __ffma2_rn(n, make_float2(-1.f, -1.f), y);
@@ -1750,7 +1751,7 @@ extern "C" nabla_status nabla_prefix_attn(nabla_heads q, int32_t B, int32_t Sq, 
   // units of work are summed in 32 bits
   const double rows = static_cast<double>(B) * (q.H / cache.H) * Sq;
   const double keys = static_cast<double>(prefix_len) + static_cast<double>(tail_cap);
-  if ((rows / 256 + B + 1) * cache.H * (keys / 128 + 2) >= 2147483648.0) return NABLA_ERR_UNSUPPORTED;
+  if ((rows / 256 + B + 1) * cache.H * (keys / 128 + 2 + kSetup) >= 2147483648.0) return NABLA_ERR_UNSUPPORTED;
   const bool part = part_o.ptr != nullptr;
   if (part != (part_lse != nullptr)) return NABLA_ERR_INVALID_ARG;
   if (part) {

@@ -540,6 +540,7 @@ extern "C" nabla_status nabla_rotary(nabla_heads q_src, nabla_heads q_dst, nabla
     }
     p.st[i].end = heads;
   }
+  if (has_q && has_k && q_dst.ptr == k_dst.ptr) return NABLA_ERR_INVALID_ARG;
   if (sdt != ddt && sdt != NABLA_F32 && ddt != NABLA_F32) return NABLA_ERR_INVALID_ARG;   // bf16 <-> fp16
   p.st[2].end = heads;
   p.heads = heads;

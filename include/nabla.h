@@ -347,7 +347,8 @@ nabla_status nabla_rotary_freqs(int32_t dim, double base, nabla_rope_scaling sca
  *   y0 = m (x0 cos a - x1 sin a),  y1 = m (x1 cos a + x0 sin a),  a = position * inv_freq
  * q_src -> q_dst and k_src -> k_dst (either pair may be absent; both pairs share their source
  *   and their destination dtype).  dtypes: bf16, fp16 or f32 on each side, not bf16 <-> fp16;
- *   computed in f32, rounded once.  No destination may overlap a source.
+ *   computed in f32, rounded once.  No destination may overlap a source or the
+ *   other destination.
  * B, grid    : S = T * Hg * W tokens; token n is (t, h, w) with n = (t*Hg + h)*W + w.  A plain
  *              sequence is T = S, Hg = W = 1.  B * S < 2^31.
  * origin     : added to the positions taken from the grid (axes == 1: n + origin.T).
@@ -424,7 +425,10 @@ nabla_status nabla_cache_append(nabla_heads k, nabla_heads v, nabla_heads q_src,
  * o          : out [B, Hq, Sq, D], q's dtype or f32.  lse: out, nullable f32 [B, Hq, Sq],
  *              natural log.  Neither may overlap an input, except that o may be part_o and
  *              lse part_lse (same address, dtype and strides).
- * Keys and values of cache slots past a sequence's length may hold anything.  The
+ * scale      : > 0.
+ * Keys and values of cache slots past a sequence's length may hold anything, and so may keys
+ * that a query does not see.  Values of the tokens within a length must be finite: a masked
+ * one enters with the weight 0, and 0 * inf is NaN.  The
  * probabilities enter the second product in the cache's 16-bit type; sums and statistics are
  * f32.  Deterministic: no atomics on data.
  * workspace  : >= nabla_prefix_workspace_bytes(B, Hq, cache.H, Sq, D) bytes, 256-byte

@@ -267,6 +267,52 @@ def test_cache_append_skips_bad_pages_and_lengths():
     assert torch.equal(vc[4], v[2, :, :16]) and torch.equal(vc[5, :, :4], v[2, :, 16:])
 
 
+def test_binding_refuses():
+    """What the C side cannot see; nothing is launched."""
+    m = nbl()
+
+    def ints(x):
+        return torch.tensor(np.asarray(x), dtype=torch.int32, device=DEV)
+    rope, rope3 = m.Rope.build(64, DEV), m.Rope.build(64, DEV, axis_dims=(32, 16, 16))
+    q = rnd((2, 4, 24, 64), torch.bfloat16, 1)
+    k = rnd((2, 2, 24, 64), torch.bfloat16, 2)
+
+    def rotary(q=q, k=k, rope=rope, **kw):
+        m.nabla_rotary(q, k, rope, **kw)
+    for kw in (dict(q=None, k=None), dict(q=q[0]), dict(k=k[:, :, :5]), dict(k=k[:1]), dict(k=k.cpu()),
+               dict(q=q.transpose(2, 3)), dict(q=q[..., ::2], k=None), dict(rope=m.Rope.build(64, "cpu")),
+               dict(rope=rope3, grid=(2, 3, 5)), dict(grid=(24,)), dict(q_out=q[:, :1].clone()[..., :32]),
+               dict(k=None, k_out=k.clone()), dict(positions=ints(np.zeros((2, 23, 1)))),
+               dict(positions=torch.zeros(2, 24, 1, device=DEV)), dict(rope=rope3, positions=ints(np.zeros((2, 24))))):
+        with pytest.raises(ValueError):
+            rotary(**kw)
+    for kw in (dict(q="q"), dict(rope=3.0), dict(q=q.double()), dict(out_dtype=2)):
+        with pytest.raises((TypeError, AttributeError)):
+            rotary(**kw)
+    for kw in (dict(q_out=q), dict(k=k.half()), dict(q_out=q.half()), dict(q_out=torch.empty_like(q[:, :2])),
+               dict(q=k, q_out=(x := torch.empty_like(k)), k_out=x)):
+        with pytest.raises(m.NablaError):
+            rotary(**kw)
+
+    kc = torch.zeros((6, 2, 16, 64), dtype=torch.bfloat16, device=DEV)
+    vc = torch.zeros_like(kc)
+    table, start = ints([[0, 1], [2, 3]]), ints([0, 0])
+
+    def append(k=k, v=k, kc=kc, vc=vc, table=table, start=start, **kw):
+        m.nabla_cache_append(k, v, kc, vc, table, start, **kw)
+    for kw in (dict(v=k[:1]), dict(v=k[:, :, :23]), dict(kc=kc.cpu()), dict(vc=vc[:5]), dict(kc=kc[:, :, ::2], vc=vc[:, :, ::2]),
+               dict(table=table[0]), dict(table=table.long()), dict(start=start[:1]), dict(counts=ints([1])),
+               dict(positions=ints(np.zeros((2, 24, 1)))), dict(q_out=q.clone(), rope=rope),
+               dict(status=torch.zeros(1, dtype=torch.int16, device=DEV)), dict(k=k[..., :32], v=k[..., :32])):
+        with pytest.raises(ValueError):
+            append(**kw)
+    for kw in (dict(k=k[:, :1], v=k[:, :1]), dict(k=k.half(), v=k.half()), dict(vc=kc), dict(q=q), dict(pos0=-1),
+               dict(rope=rope3, frame=(0, 0, 4))):
+        with pytest.raises(m.NablaError):
+            append(**kw)
+    assert not kc.any() and not vc.any()
+
+
 def test_cache_append_past_two_to_the_31_elements():
     """Pages whose element offset does not fit 32 bits."""
     m = nbl()

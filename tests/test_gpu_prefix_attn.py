@@ -229,6 +229,87 @@ def test_infinities_and_nans_of_visible_scores_stay_in_their_rows():
     assert torch.equal(o[keep], base[keep]) and torch.equal(l[keep], bl[keep])
 
 
+@pytest.mark.parametrize("name", ["one row", "wide", "chunk"])
+def test_a_nan_key_reaches_every_row_that_sees_it(name):
+    """A NaN score at each place of a tile, one head each: no path of the exponential drops it."""
+    B, Hq, Sq = {"one row": (1, 32, 1), "wide": (1, 32, 40), "chunk": (1, 32, 300)}[name]
+    pr = Problem(B=B, Hq=Hq, Hkv=32, D=64, Sq=Sq, P=384, tails=None, page=64, seed=10)
+    base, bl = pr.run()
+    k = pr.caches[0]
+    for h in range(0, 32, 2):          # even heads; the others keep their results
+        for j0 in (128, 192):
+            j = j0 + 32 * (h & 3) // 2 + h // 2 + 16 * (j0 == 192)
+            k[pr.prefix[j // 64], h, j % 64, 5] = math.nan if j0 == 128 else -math.inf
+    o, l = pr.run()
+    assert torch.isnan(o[:, 0::2]).all() and torch.isnan(l[:, 0::2]).all()
+    assert torch.equal(o[:, 1::2], base[:, 1::2]) and torch.equal(l[:, 1::2], bl[:, 1::2])
+
+
+@pytest.mark.parametrize("Sq", [5, 33, 300])
+def test_keys_that_no_query_sees_may_hold_anything(Sq):
+    """Causal, one query of each sequence: the keys behind it are masked."""
+    pr = Problem(B=2, Hq=2, Hkv=2, D=64, Sq=Sq, P=100, tails=[Sq, Sq + 40], page=16, causal=True, seed=13)
+    base, bl = pr.run()
+    for b in range(2):
+        j = pr.tails[b] - 1                     # the last query's own key: no other row sees it
+        pr.caches[0][pr.table[b][j // 16], :, j % 16] = math.nan
+    o, l = pr.run()
+    assert torch.equal(o[:, :, :-1], base[:, :, :-1]) and torch.equal(l[:, :, :-1], bl[:, :, :-1])
+    assert torch.isnan(o[:, :, -1]).all() and torch.isnan(l[:, :, -1]).all()
+
+
+@pytest.mark.parametrize("name", ["dual tails", "chunk", "chunk causal"])
+def test_bad_pages_leave_the_other_sequences_alone(name):
+    m = nbl()
+    pr = Problem(**CASES[name], seed=14)
+    base, bl = pr.run()
+    a = pr.args()
+    ws = torch.empty(m.nabla_prefix_workspace_bytes(pr.B, pr.Hq, pr.Hkv, pr.Sq, pr.D), dtype=torch.uint8, device=DEV)
+    if pr.table is not None:
+        table = pr.table.copy()
+        table[0, 0] = pr.caches[0].shape[0] + 5
+        o = torch.full_like(base, 55.0)
+        m.nabla_prefix_attn(pr.q, *pr.caches, **{**a, "tail_pages": ints(table)}, o=o, workspace=ws)
+        assert m.nabla_read_device_status(ws) == m.DEVICE_BAD_PAGE
+        assert torch.equal(o[1:], base[1:])
+    pages = pr.prefix.copy()
+    pages[1] = -2
+    m.nabla_prefix_attn(pr.q, *pr.caches, **{**a, "prefix_pages": ints(pages)}, workspace=ws)
+    assert m.nabla_read_device_status(ws) == m.DEVICE_BAD_PAGE
+    o, l = pr.run()
+    assert torch.equal(o, base) and torch.equal(l, bl)
+
+
+def test_binding_refuses():
+    """What the C side cannot see; nothing is launched."""
+    m = nbl()
+    pr = Problem(**CASES["token"], seed=15)
+    k, v = pr.caches
+    a = pr.args()
+
+    def call(q=pr.q, k=k, v=v, **kw):
+        m.nabla_prefix_attn(q, k, v, **{**a, **kw})
+    wrong = [dict(q=pr.q[0]), dict(q=pr.q.cpu()), dict(k=k.cpu()), dict(k=k[:, :, ::2]), dict(v=v[:-1]), dict(v=v.half()),
+             dict(q=pr.q[..., :64]), dict(q=pr.q.transpose(2, 3)), dict(prefix_pages=a["prefix_pages"].long()),
+             dict(prefix_pages=a["prefix_pages"][:2]), dict(tail_pages=a["tail_pages"][:2]),
+             dict(tail_pages=a["tail_pages"][0]), dict(tail_len=a["tail_len"][:3]), dict(tail_len=a["tail_len"].cpu()),
+             dict(q_len=ints([1, 1])), dict(o=pr.q[:, :, :, :64].clone()), dict(lse=torch.zeros(4, 8, 2, device=DEV)),
+             dict(lse=torch.zeros(4, 8, 1, device=DEV, dtype=F16)), dict(workspace=torch.zeros(64, device=DEV)),
+             dict(part_o=pr.q.clone(), part_lse=torch.zeros(4, 8, device=DEV))]
+    for kw in wrong:
+        with pytest.raises(ValueError):
+            call(**kw)
+    for kw in (dict(q=pr.q.double()), dict(q=[1.0]), dict(o_dtype="f32")):
+        with pytest.raises(TypeError):
+            call(**kw)
+    for kw in (dict(q=pr.q.half()), dict(tail_len=None), dict(prefix_pages=None), dict(scale=-1.0), dict(o=pr.q),
+               dict(part_o=pr.q.clone())):
+        with pytest.raises(m.NablaError):
+            call(**kw)
+    with pytest.raises(m.NablaError):
+        call(workspace=torch.zeros(256, dtype=torch.uint8, device=DEV))
+
+
 def test_bad_pages_and_lengths_are_reported():
     m = nbl()
     pr = Problem(**CASES["token"], seed=9)

@@ -110,6 +110,7 @@ def test_rotary_refuses(nb):
     assert call(qd=_view(nb, A + 64 * 64)) == INV                      # overlap
     assert call(ks=_view(nb, C3, dtype=1), kd=_view(nb, D4)) == INV    # Q and K of different dtypes
     assert call(ks=_view(nb, C3), kd=_view(nb, A)) == INV              # K's output over Q's input
+    assert call(ks=_view(nb, C3), kd=_view(nb, B2)) == INV             # one output for both
 
 
 def test_append_refuses(nb):
