@@ -114,6 +114,7 @@ struct AttnParams {
   int n_items, whole;               // whole: rounds of whole items
   int few0, few1;                   // items [few0, few1) belong to rows_attn_kernel
   int uniform;                      // length of every item of prefix_attn_kernel if the host knows it
+  int apart;                        // no CTA takes parts of two of the items left after the rounds
   int tail_rows;                    // rows of a tail part
   // workspace
   uint32_t* cta_status;
@@ -229,6 +230,18 @@ template <int kBlock>
 __device__ __forceinline__ Walk find_run(const AttnParams& p, int i0, int i1, int whole, int setup, int32_t* scratch,
                                          int uniform) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (uniform > 0 && p.apart) {    // every item has CTAs of its own
+    const int n = i1 - i0, c = static_cast<int>(blockIdx.x), ctas = static_cast<int>(gridDim.x);
+    const int i = c * n / ctas;
+    const int c0 = (i * ctas + n - 1) / n, of = ((i + 1) * ctas + n - 1) / n - c0;
+    Walk w;
+    w.round = whole > 0 ? 0 : 1 << 30;
+    w.setup = 0;
+    w.item = i0 + i;
+    w.x0 = static_cast<int>(static_cast<long long>(uniform) * (c - c0) / of);
+    w.left = static_cast<int>(static_cast<long long>(uniform) * (c - c0 + 1) / of) - w.x0;
+    return w;
+  }
   if (uniform > 0) {               // every item has that length: no scan
     const int each = uniform + setup;
     const long long total = static_cast<long long>(i1 - i0) * each;
@@ -1693,6 +1706,12 @@ nabla_status launch(const AttnParams& p, const nabla_cache& cache, uint32_t* sta
   // items of different lengths would make a round as long as its longest (uneven prompts:
   // 327 us in rounds, 261 in runs).
   a.whole = a.shared || a.uniform == 0 ? 0 : a.n_items / ctas;
+  // Items of one length that CTAs are left for: dealt out whole, each to CTAs of its own, unless
+  // runs cut anywhere are shorter even with the change of items that one of them then has.
+  // Every CTA needs a tile.
+  const int left = a.few0 - a.whole * ctas;
+  a.apart = a.uniform > 0 && left > 0 && left <= ctas && a.uniform >= (ctas + left - 1) / left &&
+            a.uniform / (ctas / left) <= static_cast<long long>(left) * a.uniform / ctas + kSetup;
   CUtensorMap mk, mv;
   if (a.few0 > 0 && (!make_map_pool(&mk, cache.k, cache) || !make_map_pool(&mv, cache.v, cache))) return NABLA_ERR_CUDA;
   cudaError_t e;
