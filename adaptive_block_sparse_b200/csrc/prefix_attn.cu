@@ -1273,28 +1273,31 @@ __global__ void __launch_bounds__(kFewThreads, 2) rows_attn_kernel(const uint16_
   }
 }
 
-// Joining the parts of split items, merging the caller's part and writing the rows; block 0
-// also gathers the CTAs' status words and looks the lengths over.
+// Joining the parts of split items, merging the caller's part and writing the rows; the last
+// block gathers the CTAs' status words and looks the lengths over (in a block of its own:
+// behind its rows' work, or before it, one block would end 3 us after the others).
 constexpr int kJoinThreads = 256;
 
 __device__ __forceinline__ void gather_status(const AttnParams& p, uint32_t* status, int ctas, int few_ctas) {
-  const int lane = threadIdx.x & 31;
+  __shared__ uint32_t found;
+  if (threadIdx.x == 0) found = 0;
+  __syncthreads();
   uint32_t w = 0;
-  for (int c = lane; c < kMaxCtas + kRowCtas; c += 32) {
-    // the words of the kernels that ran
-    const bool ran = c < kMaxCtas ? p.few0 > 0 && c < ctas : p.few1 > p.few0 && c < kMaxCtas + few_ctas;
-    if (ran && w == 0) w = p.cta_status[c];
-  }
-  for (int i = lane; i < p.B; i += 32) {
-    if (p.q_len != nullptr && queries_of(p, i) != p.q_len[i] && w == 0) w = kDevBadLength;
-    if (p.tail_pages != nullptr && tail_of(p, i) != p.tail_len[i] && w == 0) w = kDevBadLength;
-  }
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    const uint32_t v = __shfl_xor_sync(0xffffffffu, w, o);
-    if (w == 0) w = v;
+  for (int c0 = 0; c0 < kMaxCtas + kRowCtas; c0 += kJoinThreads) {
+    // the words of the kernels that ran
+    const int c = c0 + static_cast<int>(threadIdx.x);
+    const bool ran = c < kMaxCtas ? p.few0 > 0 && c < ctas : p.few1 > p.few0 && c < kMaxCtas + few_ctas;
+    const uint32_t x = ran ? p.cta_status[c] : 0u;
+    w = max(w, x);
   }
-  if (lane == 0) *status = w;
+  for (int i = threadIdx.x; i < p.B; i += kJoinThreads) {
+    if (p.q_len != nullptr && queries_of(p, i) != p.q_len[i]) w = max(w, static_cast<uint32_t>(kDevBadLength));
+    if (p.tail_pages != nullptr && tail_of(p, i) != p.tail_len[i]) w = max(w, static_cast<uint32_t>(kDevBadLength));
+  }
+  if (w != 0) atomicMax(&found, w);
+  __syncthreads();
+  if (threadIdx.x == 0) *status = found;
 }
 
 // Own mode: many rows with few parts each.  A warp joins eight rows at a time, four lanes a
@@ -1307,7 +1310,10 @@ __global__ void __launch_bounds__(kJoinThreads) own_join_kernel(const __grid_con
   constexpr int kPer = D / 32;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   wait_for_kernel_before();
-  if (blockIdx.x == 0 && blockIdx.y == 0 && warp == 0) gather_status(p, status, ctas, 0);
+  if (blockIdx.x == ctas) {
+    if (blockIdx.y == 0) gather_status(p, status, ctas, 0);
+    return;
+  }
   const int i = p.cta_done[blockIdx.x];
   if (i < 0) return;
   const Item t = item_of(p, i);
@@ -1453,10 +1459,13 @@ __global__ void __launch_bounds__(kJoinThreads) prefix_join_kernel(const __grid_
   __shared__ float acc_s[kJoinRows][kRowWarps][D];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   wait_for_kernel_before();
-  if (blockIdx.x == 0 && warp == 0) gather_status(p, status, ctas, few_ctas);
+  if (blockIdx.x == gridDim.x - 1) {
+    gather_status(p, status, ctas, few_ctas);
+    return;
+  }
   const int slot = warp / kRowWarps, sub = warp % kRowWarps;
   const long long n_rows = static_cast<long long>(p.Hkv) * p.B * p.R;
-  const long long row0 = static_cast<long long>(blockIdx.x) * kJoinRows, stride = static_cast<long long>(gridDim.x) * kJoinRows;
+  const long long row0 = static_cast<long long>(blockIdx.x) * kJoinRows, stride = static_cast<long long>(gridDim.x - 1) * kJoinRows;
   for (long long base = row0; base < n_rows; base += stride) {
     const long long id = base + slot;
     bool live = id < n_rows;
@@ -1727,10 +1736,10 @@ nabla_status launch(const AttnParams& p, const nabla_cache& cache, uint32_t* sta
   }
   if (a.shared) {
     const long long blocks = (static_cast<long long>(a.Hkv) * a.B * a.R + kJoinRows - 1) / kJoinRows;
-    e = launch_behind(true, prefix_join_kernel<D, F16>, dim3(static_cast<unsigned>(blocks < 1 << 20 ? blocks : 1 << 20)),
+    e = launch_behind(true, prefix_join_kernel<D, F16>, dim3(static_cast<unsigned>(blocks < 1 << 20 ? blocks : 1 << 20) + 1),
                       kJoinThreads, 0, st, a, status, ctas, few_ctas);
   } else {
-    e = launch_behind(true, own_join_kernel<D, F16>, dim3(ctas, kOwnJoinBlocks), kJoinThreads, 0, st, a, status, ctas);
+    e = launch_behind(true, own_join_kernel<D, F16>, dim3(ctas + 1, kOwnJoinBlocks), kJoinThreads, 0, st, a, status, ctas);
   }
   return cuda_status(e);
 }
