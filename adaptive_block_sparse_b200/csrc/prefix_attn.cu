@@ -98,7 +98,7 @@ struct AttnParams {
   int part_f32;
   const float* part_lse;
   int B, Hq, Hkv, G, Sq, R;         // R = Sq * G rows per sequence and key head
-  FastDiv div_r, div_g;
+  FastDiv div_r, div_g, div_rt, div_kv;
   // keys
   const int32_t* prefix_pages;
   const int32_t* tail_pages;
@@ -152,8 +152,9 @@ __device__ __forceinline__ Item item_of(const AttnParams& p, int i) {
   Item t;
   if (p.shared && i < p.n_prefix) {
     t.b = -1;
-    t.kvh = i / p.n_rt;
-    t.row0 = (i - t.kvh * p.n_rt) * kRows;
+    int rt;
+    t.kvh = p.div_rt.div(i, &rt);
+    t.row0 = rt * kRows;
     t.rows = min(kRows, p.B * p.R - t.row0);
     t.np = tiles(p.P);
     t.nt = 0;
@@ -164,17 +165,16 @@ __device__ __forceinline__ Item item_of(const AttnParams& p, int i) {
   if (p.shared) {
     j = i - p.n_prefix;
   } else {
-    j = i / p.n_rt;
-    rt = i - j * p.n_rt;
+    j = p.div_rt.div(i, &rt);
     if (p.causal) rt = p.n_rt - 1 - rt;       // the longest first
   }
-  t.b = j / p.Hkv;
-  t.kvh = j - t.b * p.Hkv;
+  t.b = p.div_kv.div(j, &t.kvh);
   t.row0 = rt * kRows;
   t.rows = min(kRows, p.R - t.row0);
   t.dual = !p.shared || t.rows > 128;
   const int n = queries_of(p, t.b), L = tail_of(p, t.b);
-  const int s0 = t.row0 / p.G, s1 = min((t.row0 + t.rows - 1) / p.G, n - 1);
+  int rem;
+  const int s0 = p.div_g.div(t.row0, &rem), s1 = min(p.div_g.div(t.row0 + t.rows - 1, &rem), n - 1);
   t.np = t.nt = 0;
   if (s0 < n) {
     const int v = visible(p, L, n, s1);
@@ -190,7 +190,7 @@ __device__ __forceinline__ int length_of(const Item& t) { return max(t.np + t.nt
 // inside an item's setup leaves the item to the next CTA.
 struct Walk {
   int round, item, x0, setup;
-  long long left;
+  int left;
   struct Part {
     int i;
     Item t;
@@ -209,9 +209,9 @@ struct Walk {
       o->i = item;
       o->t = item_of(p, item);
       o->total = length_of(o->t);
-      const long long end = min(static_cast<long long>(o->total + setup), x0 + left);
+      const int end = left < o->total + setup - x0 ? x0 + left : o->total + setup;
       o->x0 = max(x0 - setup, 0);
-      o->x1 = max(static_cast<int>(end) - setup, 0);
+      o->x1 = max(end - setup, 0);
       left -= end - x0;
       ++item;
       x0 = 0;
@@ -226,6 +226,13 @@ struct Walk {
 // block-wide scan of their lengths, then the thread whose items hold the run's start finds
 // it.  `scratch`: 16-byte aligned shared memory of kThreads / 32 + 8 words; all threads call it.
 constexpr int kSetup = 4, kSetupFew = 2;
+// The CTA's run when `total` units are cut into runs that differ by one unit at most, with at
+// least one each (the parts of an item are then those of neighbouring CTAs): start and length.
+__device__ __forceinline__ int run_of(int total, int* u0) {
+  const int n = static_cast<int>(gridDim.x), c = static_cast<int>(blockIdx.x), q = total / n, more = total - q * n;
+  *u0 = q * c + min(c, more);
+  return q + (c < more ? 1 : 0);
+}
 template <int kBlock>
 __device__ __forceinline__ Walk find_run(const AttnParams& p, int i0, int i1, int whole, int setup, int32_t* scratch,
                                          int uniform) {
@@ -238,22 +245,20 @@ __device__ __forceinline__ Walk find_run(const AttnParams& p, int i0, int i1, in
     w.round = whole > 0 ? 0 : 1 << 30;
     w.setup = 0;
     w.item = i0 + i;
-    w.x0 = static_cast<int>(static_cast<long long>(uniform) * (c - c0) / of);
-    w.left = static_cast<int>(static_cast<long long>(uniform) * (c - c0 + 1) / of) - w.x0;
+    const int q = uniform / of, more = uniform % of;
+    w.x0 = q * (c - c0) + min(c - c0, more);
+    w.left = q + (c - c0 < more ? 1 : 0);
     return w;
   }
   if (uniform > 0) {               // every item has that length: no scan
     const int each = uniform + setup;
-    const long long total = static_cast<long long>(i1 - i0) * each;
-    const int runs = static_cast<int>(min(total, static_cast<long long>(gridDim.x)));
-    const int run = min(static_cast<int>(blockIdx.x), runs);
-    const long long u0 = runs > 0 ? total * run / runs : 0, u1 = run < runs ? total * (run + 1) / runs : u0;
+    int u0;
     Walk w;
+    w.left = run_of((i1 - i0) * each, &u0);
     w.round = whole > 0 ? 0 : 1 << 30;
     w.setup = setup;
-    w.item = i0 + static_cast<int>(u0 / each);
-    w.x0 = static_cast<int>(u0 % each);
-    w.left = u1 - u0;
+    w.item = i0 + u0 / each;
+    w.x0 = u0 % each;
     return w;
   }
   int32_t* sums = scratch + 4;
@@ -276,12 +281,10 @@ __device__ __forceinline__ Walk find_run(const AttnParams& p, int i0, int i1, in
     if (w < warp) before += sums[w];
     total += sums[w];
   }
-  // every run has at least one unit, so the parts of an item are those of neighbouring CTAs
-  const int runs = min(total, static_cast<int>(gridDim.x)), run = min(static_cast<int>(blockIdx.x), runs);
-  const long long u0 = runs > 0 ? static_cast<long long>(total) * run / runs : 0;
-  const long long u1 = run < runs ? static_cast<long long>(total) * (run + 1) / runs : u0;
+  int u0;
+  const int mine = run_of(total, &u0);
   int at = before + inc - sum;                 // units before this thread's items
-  if (u1 > u0 && u0 >= at && u0 < at + sum) {
+  if (mine > 0 && u0 >= at && u0 < at + sum) {
     int i = a, len = 0;
     for (; i < b; ++i) {
       len = length_of(item_of(p, i0 + i)) + setup;
@@ -289,8 +292,8 @@ __device__ __forceinline__ Walk find_run(const AttnParams& p, int i0, int i1, in
       at += len;
     }
     scratch[0] = i0 + i;
-    scratch[1] = static_cast<int>(u0 - at);
-    scratch[2] = static_cast<int>(u1 - u0);
+    scratch[1] = u0 - at;
+    scratch[2] = mine;
   }
   __syncthreads();
   Walk w;
@@ -1079,7 +1082,7 @@ __global__ void __launch_bounds__(kFewThreads, 2) rows_attn_kernel(const uint16_
       }
     };
     auto load = [&](int j) {                       // group j of the warp into stage j % kStages
-      if ((j & 31) == 0) look_up(j);
+      if (j > 0 && (j & 31) == 0) look_up(j);
       const int id = __shfl_sync(0xffffffffu, ids, j & 31);
       if (j < mine) {
         const int key = key0 + (warp + j * kFewWarps) * kGroup;
@@ -1099,10 +1102,9 @@ __global__ void __launch_bounds__(kFewThreads, 2) rows_attn_kernel(const uint16_
       }
       asm volatile("cp.async.commit_group;" ::: "memory");
     };
-#pragma unroll
-    for (int j = 0; j < C::kStages - 1; ++j) load(j);
-
-    // The thread's two rows: keys they see, and their Q in A-operand registers.
+    look_up(0);
+    // The thread's two rows: keys they see, and their Q in A-operand registers (requested
+    // before the first keys, whose traffic would hold it up).
     int lim[2];
     uint32_t qf[D / 16][4];
 #pragma unroll
@@ -1127,6 +1129,8 @@ __global__ void __launch_bounds__(kFewThreads, 2) rows_attn_kernel(const uint16_
         qf[c][2 + e] = src != nullptr ? *reinterpret_cast<const uint32_t*>(src + c * 16 + 8) : 0u;
       }
     }
+#pragma unroll
+    for (int j = 0; j < C::kStages - 1; ++j) load(j);
     float o[D / 8][4];
 #pragma unroll
     for (int c = 0; c < D / 8; ++c)
@@ -1431,9 +1435,8 @@ struct PartList {
   __device__ __forceinline__ long long at(int j) const { return j == 0 ? r0 : r1 + static_cast<long long>(j - 1) * step; }
 };
 
-__device__ __forceinline__ PartList parts_of(const AttnParams& p, int i, int lrow, int ctas) {
+__device__ __forceinline__ PartList parts_of(const AttnParams& p, int i, int first, int last, int lrow, int ctas) {
   PartList l;
-  const int first = p.first[i], last = p.last[i];
   l.n = 0;
   const bool few = i >= p.few0 && i < p.few1;
   if (first < 0 || last < first || last >= (few ? kRowCtas : ctas)) return l;       // only after a wait gave up
@@ -1474,14 +1477,22 @@ __global__ void __launch_bounds__(kJoinThreads) prefix_join_kernel(const __grid_
     l0.n = l1.n = 0;
     if (live) {
       const int per = p.B * p.R;
-      kvh = static_cast<int>(id / per);
+      kvh = n_rows < 1LL << 31 ? static_cast<int>(static_cast<uint32_t>(id) / static_cast<uint32_t>(per))
+                               : static_cast<int>(id / per);
       const int rg = static_cast<int>(id - static_cast<long long>(kvh) * per);
       b = p.div_r.div(rg, &rr);
+      const int rt = rg / kRows, i0 = kvh * p.n_rt + rt, i1 = p.n_prefix + b * p.Hkv + kvh;
+      int f0 = -1, e0 = -1, f1 = -1, e1 = -1;            // (all requested at once)
       if (p.n_prefix > 0) {
-        const int rt = rg / kRows;
-        l0 = parts_of(p, kvh * p.n_rt + rt, rg - rt * kRows, ctas);
+        f0 = p.first[i0];
+        e0 = p.last[i0];
       }
-      if (p.tail_pages != nullptr) l1 = parts_of(p, p.n_prefix + b * p.Hkv + kvh, rr, ctas);
+      if (p.tail_pages != nullptr) {
+        f1 = p.first[i1];
+        e1 = p.last[i1];
+      }
+      l0 = parts_of(p, i0, f0, e0, rg - rt * kRows, ctas);
+      l1 = parts_of(p, i1, f1, e1, rr, ctas);
       s = p.div_g.div(rr, &gh);
       live = s < queries_of(p, b);
     }
@@ -1844,6 +1855,8 @@ extern "C" nabla_status nabla_prefix_attn(nabla_heads q, int32_t B, int32_t Sq, 
   p.scale_log2 = scale * 1.4426950408889634f;
   p.shared = plan.shared;
   p.n_rt = static_cast<int>(plan.n_rt);
+  p.div_rt.init(p.n_rt);
+  p.div_kv.init(cache.H);
   // without tails (or without a prefix) shared mode has only the other kind of items
   p.n_prefix = plan.shared && (prefix_len > 0 || !tail_pages) ? static_cast<int>(plan.n_prefix) : 0;
   p.n_items = plan.shared ? p.n_prefix + (tail_pages ? static_cast<int>(plan.n_tail) : 0) : static_cast<int>(plan.n_items);
