@@ -964,21 +964,31 @@ __global__ void __launch_bounds__(kThreads, 1)
           *reinterpret_cast<float4*>(stage + lane * 128 + ((i ^ (lane & 7)) << 4)) =
               make_float4(a[4 * i], a[4 * i + 1], a[4 * i + 2], a[4 * i + 3]);
         __syncwarp();
+        float4 f[8];
 #pragma unroll
         for (int it = 0; it < 8; ++it) {
           const int rr = 4 * it + (lane >> 3);
-          float4 f = *reinterpret_cast<const float4*>(stage + rr * 128 + ((ch ^ (rr & 7)) << 4));
-          if (merge) {
-            const float w = __shfl_sync(0xffffffffu, pw, rr);
-            f.x += w * y[it].x; f.y += w * y[it].y; f.z += w * y[it].z; f.w += w * y[it].w;
+          f[it] = *reinterpret_cast<const float4*>(stage + rr * 128 + ((ch ^ (rr & 7)) << 4));
+        }
+        if (merge) {
+#pragma unroll
+          for (int it = 0; it < 8; ++it) {
+            const float w = __shfl_sync(0xffffffffu, pw, 4 * it + (lane >> 3));
+            f[it].x += w * y[it].x; f[it].y += w * y[it].y; f[it].z += w * y[it].z; f[it].w += w * y[it].w;
           }
-          if (hows >> (2 * it) & 1) {
-            if (to_f32)
-              *reinterpret_cast<float4*>((whole ? static_cast<float*>(p.o) : p.part_acc) + to[it] + d0) = f;
-            else
-              *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.o) + to[it] + d0) =
-                  make_uint2(pack2<F16>(f.x, f.y), pack2<F16>(f.z, f.w));
-          }
+        }
+        if (to_f32) {
+          float* base = (whole ? static_cast<float*>(p.o) : p.part_acc) + d0;
+#pragma unroll
+          for (int it = 0; it < 8; ++it)
+            if (hows >> (2 * it) & 1) *reinterpret_cast<float4*>(base + to[it]) = f[it];
+        } else {
+          uint16_t* base = static_cast<uint16_t*>(p.o) + d0;
+#pragma unroll
+          for (int it = 0; it < 8; ++it)
+            if (hows >> (2 * it) & 1)
+              *reinterpret_cast<uint2*>(base + to[it]) =
+                  make_uint2(pack2<F16>(f[it].x, f[it].y), pack2<F16>(f[it].z, f[it].w));
         }
       }
     }
