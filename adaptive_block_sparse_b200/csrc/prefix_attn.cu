@@ -56,8 +56,8 @@ constexpr int kKeys = 128;                // keys per tile
 constexpr int kRows = 256;                // query rows per item
 constexpr int kLaunchRegs = 168;
 constexpr int kPolyPairs = 2;             // of 8 pairs of weights, by poly_exp2
-constexpr int kRegProducer = 56;
-constexpr int kRegSoftmax = 224;
+constexpr int kRegProducer = 72;
+constexpr int kRegSoftmax = 216;
 static_assert(128 * kRegProducer + 256 * kRegSoftmax <= kThreads * kLaunchRegs,
               "register split exceeds the block's launch budget");
 
