@@ -50,8 +50,8 @@ namespace {
 constexpr int kThreads = 384;
 constexpr int kSoftmaxWarp0 = 4;          // warps 4..7 = slot 0, 8..11 = slot 1
 constexpr int kMaxCtas = 148;
-constexpr int kRowCtas = 2 * kMaxCtas;    // CTAs of rows_attn_kernel
-constexpr int kFewRows = 16;              // most rows of an item of rows_attn_kernel
+constexpr int kRowCtas = 2 * kMaxCtas;    // most CTAs of rows_attn_kernel
+constexpr int kFewRows = 16;              // most rows of an item with few rows
 constexpr int kKeys = 128;                // keys per tile
 constexpr int kRows = 256;                // query rows per item
 constexpr int kLaunchRegs = 168;
@@ -112,9 +112,8 @@ struct AttnParams {
   int n_rt;                         // row tiles: of a sequence (own), of the batch (shared)
   int n_prefix;                     // prefix items (shared mode)
   int n_items, whole;               // whole: rounds of whole items
-  int few0, few1;                   // items [few0, few1) belong to rows_attn_kernel
-  int uniform;                      // length of every item of prefix_attn_kernel if the host knows it
-  int apart;                        // no CTA takes parts of two of the items left after the rounds
+  int few0, few1;                   // items [few0, few1) have few rows
+  int uniform;                      // length of every item before few0 if the host knows it
   int tail_rows;                    // rows of a tail part
   // workspace
   uint32_t* cta_status;
@@ -222,53 +221,25 @@ struct Walk {
   }
 };
 
-// The CTA's run of units among items [i0, i1), which are cut into runs of equal length: a
-// block-wide scan of their lengths, then the thread whose items hold the run's start finds
-// it.  `scratch`: 16-byte aligned shared memory of kThreads / 32 + 8 words; all threads call it.
+// Items [i0, i1) are cut into runs of equal length, one per CTA of those that share them.  The
+// units before a thread's items and in them, by a block-wide scan of the items' lengths.
+// `scratch`: 16-byte aligned shared memory of kBlock / 32 + 4 words; all threads call it.
 constexpr int kSetup = 4, kSetupFew = 2;
-// The CTA's run when `total` units are cut into runs that differ by one unit at most, with at
-// least one each (the parts of an item are then those of neighbouring CTAs): start and length.
-__device__ __forceinline__ int run_of(int total, int* u0) {
-  const int n = static_cast<int>(gridDim.x), c = static_cast<int>(blockIdx.x), q = total / n, more = total - q * n;
-  *u0 = q * c + min(c, more);
-  return q + (c < more ? 1 : 0);
-}
+struct Units {
+  int a, b, at, sum, total;
+};
 template <int kBlock>
-__device__ __forceinline__ Walk find_run(const AttnParams& p, int i0, int i1, int whole, int setup, int32_t* scratch,
-                                         int uniform) {
+__device__ __forceinline__ Units scan_units(const AttnParams& p, int i0, int i1, int setup, int32_t* scratch) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (uniform > 0 && p.apart) {    // every item has CTAs of its own
-    const int n = i1 - i0, c = static_cast<int>(blockIdx.x), ctas = static_cast<int>(gridDim.x);
-    const int i = c * n / ctas;
-    const int c0 = (i * ctas + n - 1) / n, of = ((i + 1) * ctas + n - 1) / n - c0;
-    Walk w;
-    w.round = whole > 0 ? 0 : 1 << 30;
-    w.setup = 0;
-    w.item = i0 + i;
-    const int q = uniform / of, more = uniform % of;
-    w.x0 = q * (c - c0) + min(c - c0, more);
-    w.left = q + (c - c0 < more ? 1 : 0);
-    return w;
-  }
-  if (uniform > 0) {               // every item has that length: no scan
-    const int each = uniform + setup;
-    int u0;
-    Walk w;
-    w.left = run_of((i1 - i0) * each, &u0);
-    w.round = whole > 0 ? 0 : 1 << 30;
-    w.setup = setup;
-    w.item = i0 + u0 / each;
-    w.x0 = u0 % each;
-    return w;
-  }
   int32_t* sums = scratch + 4;
   if (threadIdx.x == 0) scratch[0] = scratch[1] = scratch[2] = 0;
-  const int n = i1 - i0;
-  const int per = (n + kBlock - 1) / kBlock;
-  const int a = min(static_cast<int>(threadIdx.x) * per, n), b = min(a + per, n);
-  int sum = 0;
-  for (int i = a; i < b; ++i) sum += length_of(item_of(p, i0 + i)) + setup;
-  int inc = sum;
+  const int n = i1 - i0, per = (n + kBlock - 1) / kBlock;
+  Units u;
+  u.a = min(static_cast<int>(threadIdx.x) * per, n);
+  u.b = min(u.a + per, n);
+  u.sum = u.total = 0;
+  for (int i = u.a; i < u.b; ++i) u.sum += length_of(item_of(p, i0 + i)) + setup;
+  int inc = u.sum;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const int v = __shfl_up_sync(0xffffffffu, inc, o);
@@ -276,18 +247,31 @@ __device__ __forceinline__ Walk find_run(const AttnParams& p, int i0, int i1, in
   }
   if (lane == 31) sums[warp] = inc;
   __syncthreads();
-  int before = 0, total = 0;
+  u.at = inc - u.sum;
   for (int w = 0; w < kBlock / 32; ++w) {
-    if (w < warp) before += sums[w];
-    total += sums[w];
+    if (w < warp) u.at += sums[w];
+    u.total += sums[w];
   }
+  return u;
+}
+
+// Run c of n when `total` units are cut into runs that differ by one unit at most, with at
+// least one each (the parts of an item are then those of neighbouring CTAs): start and length.
+__device__ __forceinline__ int run_of(int total, int c, int n, int* u0) {
+  const int q = total / n, more = total - q * n;
+  *u0 = q * c + min(c, more);
+  return q + (c < more ? 1 : 0);
+}
+
+// The thread whose items hold the run's start finds it (all threads call).
+__device__ __forceinline__ Walk find_run(const AttnParams& p, const Units& u, int i0, int c, int n, int setup,
+                                         int32_t* scratch) {
   int u0;
-  const int mine = run_of(total, &u0);
-  int at = before + inc - sum;                 // units before this thread's items
-  if (mine > 0 && u0 >= at && u0 < at + sum) {
-    int i = a, len = 0;
-    for (; i < b; ++i) {
-      len = length_of(item_of(p, i0 + i)) + setup;
+  const int mine = run_of(u.total, c, n, &u0);
+  if (mine > 0 && u0 >= u.at && u0 < u.at + u.sum) {
+    int i = u.a, at = u.at;
+    for (; i < u.b; ++i) {
+      const int len = length_of(item_of(p, i0 + i)) + setup;
       if (u0 < at + len) break;
       at += len;
     }
@@ -297,11 +281,38 @@ __device__ __forceinline__ Walk find_run(const AttnParams& p, int i0, int i1, in
   }
   __syncthreads();
   Walk w;
-  w.round = whole > 0 ? 0 : 1 << 30;
+  w.round = 1 << 30;
   w.setup = setup;
   w.item = scratch[0];
   w.x0 = scratch[1];
   w.left = scratch[2];
+  return w;
+}
+
+// n items of `len` tiles and `ctas` CTAs: every item gets CTAs of its own (each with a tile at
+// least), unless runs cut anywhere are shorter even with the change of items in some of them.
+__device__ __forceinline__ bool items_apart(int len, int n, int ctas) {
+  if (n > ctas || len < (ctas + n - 1) / n) return false;
+  return len / (ctas / n) <= static_cast<int>(static_cast<float>(n) * len / ctas) + kSetup;
+}
+
+// The same for items i0 .. i0 + n - 1 of one length.
+__device__ __forceinline__ Walk find_run_of_equals(int len, int i0, int n, int c, int ctas) {
+  Walk w;
+  w.round = 1 << 30;
+  if (items_apart(len, n, ctas)) {
+    const int i = c * n / ctas;
+    const int c0 = (i * ctas + n - 1) / n, of = ((i + 1) * ctas + n - 1) / n - c0;
+    w.setup = 0;
+    w.item = i0 + i;
+    w.left = run_of(len, c - c0, of, &w.x0);
+  } else {
+    int u0;
+    w.setup = kSetup;
+    w.left = run_of(n * (len + kSetup), c, ctas, &u0);
+    w.item = i0 + u0 / (len + kSetup);
+    w.x0 = u0 % (len + kSetup);
+  }
   return w;
 }
 
@@ -313,7 +324,8 @@ struct Bars {
   uint64_t o_done[2], o_free[2];    // the part's last P V landed / the accumulator was read
   uint64_t drain;
   uint32_t tmem;
-  alignas(16) int32_t scratch[kThreads / 32 + 8];
+  alignas(16) int32_t scratch[kThreads / 32 + 4];
+  float stat[8][16][2];             // few_rows()
 };
 
 template <int D>
@@ -404,9 +416,307 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
   return F16 ? pack_f16x2(a, b) : pack_bf16x2(a, b);
 }
 
+// ------------------------------------------------------------------------------------
+// Items of at most 16 rows.  Bound by the cache's bytes, and by latency when those are few:
+// a 128-row MMA tile would be mostly padding and its pipeline (8 us from launch to result)
+// longer than the work.  The warps of a CTA take a run of units as above; each of kWarps warps
+// streams every kWarps-th group of 16 keys through its own ring in shared memory (cp.async, 24
+// KB in flight a warp, 192 KB an SM), multiplies with m16n8k16 MMAs (the rows as M, so the
+// scores' registers are the second product's A operand), and keeps m, l and O in registers.
+// The warps' results are joined through shared memory at the part's end.
+//
+// A call with such items only runs rows_attn_kernel (two CTAs of four warps an SM); one with a
+// long prefix for many rows as well gives them some of the CTAs of prefix_attn_kernel, whose
+// softmax warps do the same: one kernel fills the GPU, where two in turn each ramped up and
+// ran out (32 tokens over 32768: @@ us, 63.6 us in turn).
+// ------------------------------------------------------------------------------------
+constexpr int kFewThreads = 128;
+constexpr int kGroup = 16;                 // keys of a ring stage
+
+template <int D>
+struct FewCfg {
+  static constexpr int kHalf = kGroup * D * 2;           // bytes of K (or V) of a group
+  static constexpr int kStages = D == 128 ? 3 : 6;
+  static constexpr int kWarpBytes = kStages * 2 * kHalf;
+  static constexpr int kSmemBytes = kFewThreads / 32 * kWarpBytes;
+  static_assert(kFewRows * (D + 4) * 4 <= kWarpBytes, "the joined results reuse the rings");
+};
+
+__device__ __forceinline__ void ldmatrix_x4(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr));
+}
+__device__ __forceinline__ void ldmatrix_x4_trans(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr));
+}
+template <bool F16>
+__device__ __forceinline__ void mma_16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  if constexpr (F16)
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  else
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// 16 bytes, or zeros
+__device__ __forceinline__ void cp_async16_or_zero(uint32_t dst, const void* src, bool read) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(read ? 16 : 0) : "memory");
+}
+
+// The CTA's parts.  Barrier kBar is the calling warps'; `warp` counts among them.
+template <int D, bool F16, int kWarps, int kBar>
+__device__ __forceinline__ void few_rows(const AttnParams& p, Walk walk, int cta, const uint16_t* __restrict__ k_pool,
+                                         const uint16_t* __restrict__ v_pool, unsigned char* smem,
+                                         float (*stat)[kFewRows][2], int warp, uint32_t* status) {
+  using C = FewCfg<D>;
+  const int lane = threadIdx.x & 31;
+  auto sync = [] { asm volatile("barrier.cta.sync %0, %1;" ::"n"(kBar), "n"(kWarps * 32) : "memory"); };
+  const uint32_t ring = smem_u32(smem) + warp * C::kWarpBytes;
+  constexpr float kBias = F16 ? 7.0f : 0.0f;       // as in prefix_attn_kernel
+  constexpr int kChunks = D / 8;                   // 16-byte pieces of a row
+  constexpr int kRowsPerCopy = 32 / kChunks;       // rows that one copy of the warp covers
+  const int c_row = lane / kChunks, c_ch = lane % kChunks;
+  const int q0 = lane >> 2, kq = (lane & 3) * 2;   // fragment row (and row + 8), column pair
+  Walk::Part part;
+  while (walk.next(p, &part)) {
+    const Item& t = part.t;
+    const bool pre = t.b < 0;
+    const int L = pre ? p.P : tail_of(p, t.b);
+    const int32_t* list = pre ? p.prefix_pages : p.tail_pages + static_cast<long long>(t.b) * p.tail_width;
+    const int key0 = part.x0 * kKeys;
+    const int key1 = part.n > 0 ? min(part.x1 * kKeys, L) : key0;
+    const int groups = (key1 - key0 + kGroup - 1) / kGroup;
+    const int mine = groups > warp ? (groups - warp + kWarps - 1) / kWarps : 0;
+    // page numbers of the warp's groups, 32 at a time, one per lane
+    int ids = 0;
+    auto look_up = [&](int j) {                    // groups j .. j + 31 of the warp
+      const int key = key0 + (warp + (j + lane) * kWarps) * kGroup;
+      ids = -1;
+      if (j + lane < mine) {
+        const int id = __ldg(list + (key >> p.page_shift));
+        if (id < 0 || id >= p.n_pages) record_status(status, kDevBadPage);
+        else ids = id;
+      }
+    };
+    auto load = [&](int j) {                       // group j of the warp into stage j % kStages
+      if (j > 0 && (j & 31) == 0) look_up(j);
+      const int id = __shfl_sync(0xffffffffu, ids, j & 31);
+      if (j < mine) {
+        const int key = key0 + (warp + j * kWarps) * kGroup;
+        const long long off = static_cast<long long>(max(id, 0)) * p.Hkv * p.page * D +
+                              (static_cast<long long>(t.kvh) * p.page + (key & (p.page - 1))) * D;
+        const uint32_t st = ring + (j % C::kStages) * 2 * C::kHalf;
+#pragma unroll
+        for (int i = 0; i < kGroup / kRowsPerCopy; ++i) {
+          const int r = i * kRowsPerCopy + c_row;
+          const uint32_t dst = st + r * D * 2 + ((c_ch ^ (r & 7)) << 4);
+          // a bad page, and slots past the length, are read as zeros
+          const bool read = id >= 0 && key + r < key1;
+          const long long src = off + (read ? r * D + c_ch * 8 : 0);
+          cp_async16_or_zero(dst, k_pool + src, read);
+          cp_async16_or_zero(dst + C::kHalf, v_pool + src, read);
+        }
+      }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    look_up(0);
+    // The thread's two rows: keys they see, and their Q in A-operand registers (requested
+    // before the first keys, whose traffic would hold it up).
+    int lim[2];
+    uint32_t qf[D / 16][4];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int r = q0 + 8 * e;
+      const uint16_t* src = nullptr;
+      lim[e] = 0;
+      if (r < t.rows) {
+        int b = t.b, rr = t.row0 + r, g;
+        if (b < 0) b = p.div_r.div(rr, &rr);
+        const int s = p.div_g.div(rr, &g);
+        const int n = queries_of(p, b);
+        if (s < n) {
+          const int v = visible(p, tail_of(p, b), n, s);
+          lim[e] = pre ? min(v, p.P) : v - p.P;
+          src = static_cast<const uint16_t*>(p.q) + b * p.q_b + (t.kvh * p.G + g) * p.q_h + s * p.q_s + kq;
+        }
+      }
+#pragma unroll
+      for (int c = 0; c < D / 16; ++c) {
+        qf[c][e] = src != nullptr ? *reinterpret_cast<const uint32_t*>(src + c * 16) : 0u;
+        qf[c][2 + e] = src != nullptr ? *reinterpret_cast<const uint32_t*>(src + c * 16 + 8) : 0u;
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < C::kStages - 1; ++j) load(j);
+    float o[D / 8][4];
+#pragma unroll
+    for (int c = 0; c < D / 8; ++c)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) o[c][i] = 0.f;
+    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+    for (int j = 0; j < mine; ++j) {
+      asm volatile("cp.async.wait_group %0;" ::"n"(C::kStages - 2) : "memory");
+      __syncwarp();                                // every lane's copies of group j; stage j - 1 is read
+      load(j + C::kStages - 1);
+      const uint32_t st = ring + (j % C::kStages) * 2 * C::kHalf;
+      const int key = key0 + (warp + j * kWarps) * kGroup;
+      float sc[2][4];
+#pragma unroll
+      for (int n = 0; n < 2; ++n)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) sc[n][i] = 0.f;
+#pragma unroll
+      for (int n = 0; n < 2; ++n) {
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) {         // 32 channels: four 8 x 8 matrices
+          const int r = n * 8 + (lane & 7), ch = c * 4 + (lane >> 3);
+          uint32_t kf[4];
+          ldmatrix_x4(kf, st + r * D * 2 + ((ch ^ (r & 7)) << 4));
+          mma_16816<F16>(sc[n], qf[2 * c], kf[0], kf[1]);
+          mma_16816<F16>(sc[n], qf[2 * c + 1], kf[2], kf[3]);
+        }
+      }
+      float mx[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+      for (int n = 0; n < 2; ++n)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int e = i >> 1;
+          if (key + n * 8 + kq + (i & 1) >= lim[e]) sc[n][i] = -INFINITY;
+          mx[e] = fmaxf(mx[e], sc[n][i]);
+        }
+      float factor[2] = {1.f, 1.f};
+      bool rescale = false;
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], 1));
+        mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], 2));
+        const float rm = mx[e] * p.scale_log2 - kBias;
+        if (mx[e] != -INFINITY && rm > m[e] + 8.0f) {
+          if (m[e] != -INFINITY) {
+            factor[e] = fast_exp2(m[e] - rm);
+            rescale = true;
+          }
+          m[e] = rm;
+        }
+      }
+      if (__any_sync(0xffffffffu, rescale)) {
+#pragma unroll
+        for (int c = 0; c < D / 8; ++c)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) o[c][i] *= factor[i >> 1];
+        l[0] *= factor[0];
+        l[1] *= factor[1];
+      }
+      uint32_t pf[4];
+#pragma unroll
+      for (int n = 0; n < 2; ++n)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const float neg = m[e] == -INFINITY ? 0.f : -m[e];
+          const float x = fast_exp2(fmaf(sc[n][2 * e], p.scale_log2, neg));
+          const float y = fast_exp2(fmaf(sc[n][2 * e + 1], p.scale_log2, neg));
+          l[e] += x + y;
+          pf[2 * n + e] = pack2<F16>(x, y);
+        }
+#pragma unroll
+      for (int c = 0; c < D / 16; ++c) {           // 16 channels: two tiles of 8, two halves of the keys
+        const int r = (lane & 7) + (lane & 8), ch = c * 2 + (lane >> 4);
+        uint32_t vf[4];
+        ldmatrix_x4_trans(vf, st + C::kHalf + r * D * 2 + ((ch ^ (r & 7)) << 4));
+        mma_16816<F16>(o[2 * c], pf, vf[0], vf[1]);
+        mma_16816<F16>(o[2 * c + 1], pf, vf[2], vf[3]);
+      }
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      l[e] += __shfl_xor_sync(0xffffffffu, l[e], 1);
+      l[e] += __shfl_xor_sync(0xffffffffu, l[e], 2);
+    }
+    // Join the warps (the rings are free now): rows of D values, then m and l.
+    sync();
+    constexpr int kPitch = D + 4;
+    float* acc = reinterpret_cast<float*>(smem);
+#pragma unroll
+    for (int c = 0; c < D / 8; ++c) {
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+        *reinterpret_cast<float2*>(acc + (warp * kFewRows + q0 + 8 * e) * kPitch + c * 8 + kq) =
+            make_float2(o[c][2 * e], o[c][2 * e + 1]);
+    }
+    if ((lane & 3) == 0) {
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        stat[warp][q0 + 8 * e][0] = m[e];
+        stat[warp][q0 + 8 * e][1] = l[e];
+      }
+    }
+    sync();
+    if (warp == 0 && lane == 0) {
+      if (part.x0 == 0) p.first[part.i] = cta;
+      if (part.x1 == part.total) p.last[part.i] = cta;
+    }
+    constexpr int kPerRow = 32 * kWarps / kFewRows;                 // threads a row
+    const int thread = warp * 32 + lane, r = thread / kPerRow;
+    if (r < t.rows) {
+      int b = t.b, rr = t.row0 + r, g;
+      if (b < 0) b = p.div_r.div(rr, &rr);
+      const int s = p.div_g.div(rr, &g);
+      if (s < queries_of(p, b)) {
+        float top = -INFINITY, sum = 0.f, w[kWarps];
+#pragma unroll
+        for (int k = 0; k < kWarps; ++k) top = fmaxf(top, stat[k][r][0]);
+#pragma unroll
+        for (int k = 0; k < kWarps; ++k) {
+          const float lk = stat[k][r][1];
+          w[k] = lk == 0.f ? 0.f : exp2f(stat[k][r][0] - top);
+          sum += lk == 0.f ? 0.f : w[k] * lk;
+        }
+        const long long row = p.few_base + static_cast<long long>(part.i - p.few0 + cta) * kFewRows + r;
+        const float inv = sum == 0.f ? 0.f : 1.f / sum;
+        if (thread % kPerRow == 0) p.part_l[row] = sum == 0.f ? -INFINITY : top + log2f(sum);
+#pragma unroll
+        for (int i = 0; i < D / (4 * kPerRow); ++i) {
+          const int d = 4 * (thread % kPerRow + i * kPerRow);
+          float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+          for (int k = 0; k < kWarps; ++k) {
+            const float4 x = *reinterpret_cast<const float4*>(acc + (k * kFewRows + r) * kPitch + d);
+            f.x += w[k] * x.x; f.y += w[k] * x.y; f.z += w[k] * x.z; f.w += w[k] * x.w;
+          }
+          *reinterpret_cast<float4*>(p.part_acc + row * D + d) = make_float4(f.x * inv, f.y * inv, f.z * inv, f.w * inv);
+        }
+      }
+    }
+    sync();
+  }
+}
+
+template <int D, bool F16>
+__global__ void __launch_bounds__(kFewThreads, 2) rows_attn_kernel(const uint16_t* __restrict__ k_pool,
+                                                                    const uint16_t* __restrict__ v_pool,
+                                                                    const __grid_constant__ AttnParams p) {
+  extern __shared__ __align__(16) unsigned char smem[];
+  __shared__ __align__(16) int32_t scratch[kFewThreads / 32 + 4];
+  __shared__ float stat[kFewThreads / 32][kFewRows][2];
+  uint32_t* status = p.cta_status + blockIdx.x;
+  next_kernel_may_start();
+  if (threadIdx.x == 0) *status = 0;
+  const Walk walk = find_run(p, scan_units<kFewThreads>(p, p.few0, p.few1, kSetupFew, scratch), p.few0, blockIdx.x,
+                             gridDim.x, kSetupFew, scratch);
+  few_rows<D, F16, kFewThreads / 32, 0>(p, walk, blockIdx.x, k_pool, v_pool, smem, stat, threadIdx.x >> 5, status);
+}
+
 template <int D, bool F16>
 __global__ void __launch_bounds__(kThreads, 1)
     prefix_attn_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
+                       const uint16_t* __restrict__ k_pool, const uint16_t* __restrict__ v_pool,
                        const __grid_constant__ AttnParams p) {
   using C = Cfg<D>;
   extern __shared__ unsigned char smem_raw[];
@@ -441,8 +751,25 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_alloc(&B.tmem, 512);
     tmem_relinquish();
   }
-  Walk walk = find_run<kThreads>(p, p.whole * static_cast<int>(gridDim.x), p.few0, p.whole, kSetup, B.scratch,
-                                  p.uniform);
+  // The CTA's run: among the long items, or, where a call has items of few rows as well, among
+  // those; each kind gets a share of the CTAs by its units.
+  const int c = blockIdx.x, ctas = gridDim.x;
+  const int i0 = p.whole * ctas, n_left = p.few0 - i0;
+  Walk walk;
+  int few_cta = -1;                 // its index among the CTAs of the items of few rows
+  if (p.few1 > p.few0) {
+    const Units u = scan_units<kThreads>(p, p.few0, p.few1, kSetupFew, B.scratch);
+    const float long_units = static_cast<float>(n_left) * (p.uniform + kSetup);
+    const int n_long = min(max(static_cast<int>(ctas * long_units / (long_units + u.total) + 0.5f), 1), ctas - 1);
+    if (c >= n_long) few_cta = c - n_long;
+    if (few_cta >= 0) walk = find_run(p, u, p.few0, few_cta, ctas - n_long, kSetupFew, B.scratch);
+    else walk = find_run_of_equals(p.uniform, i0, n_left, c, n_long);
+  } else if (p.uniform > 0 && n_left > 0) {
+    walk = find_run_of_equals(p.uniform, i0, n_left, c, ctas);
+  } else {
+    walk = find_run(p, scan_units<kThreads>(p, i0, p.few0, kSetup, B.scratch), i0, c, ctas, kSetup, B.scratch);
+  }
+  if (p.whole > 0) walk.round = 0;
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -451,6 +778,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp < kSoftmaxWarp0) {
     reg_dealloc<kRegProducer>();
+    if (few_cta >= 0) walk.left = 0;       // few_rows() is the other warps' work
     if (warp == 0) {
       // ------------------------------------------------------------------ K and V tiles
       // A tile is K then V, in successive stages of one ring.  Its pages (or, for large
@@ -667,6 +995,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else {
     reg_alloc<kRegSoftmax>();
+    if (few_cta >= 0) {
+      few_rows<D, F16, 8, 5>(p, walk, few_cta, k_pool, v_pool, smem, B.stat, warp - kSoftmaxWarp0, status);
+      walk.left = 0;
+    }
     // -------------------------------------------------------------------- softmax of a slot
     const int slot = (warp - kSoftmaxWarp0) >> 2;
     const int row = ((warp - kSoftmaxWarp0) & 3) * 32 + lane;       // TMEM lane
@@ -1000,291 +1332,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
-  // The join kernel waits for this one only: end after rows_attn_kernel.
-  if (threadIdx.x == 0) wait_for_kernel_before();
-}
-
-// ------------------------------------------------------------------------------------
-// Items of at most 16 rows.  Bound by the cache's bytes, and by latency when those are few:
-// a 128-row MMA tile would be mostly padding and its pipeline (8 us from launch to result)
-// longer than the work.  A CTA of four warps takes a run of units as above; a warp streams
-// every fourth group of 16 keys through its own ring in shared memory (cp.async, 24 KB in
-// flight a warp, 192 KB an SM), multiplies with m16n8k16 MMAs (the rows as M, so the
-// scores' registers are the second product's A operand), and keeps m, l and O in registers.
-// The four warps' results are joined through shared memory at the part's end.
-// ------------------------------------------------------------------------------------
-constexpr int kFewThreads = 128;
-constexpr int kFewWarps = kFewThreads / 32;
-constexpr int kGroup = 16;                 // keys of a ring stage
-
-template <int D>
-struct FewCfg {
-  static constexpr int kHalf = kGroup * D * 2;           // bytes of K (or V) of a group
-  static constexpr int kStages = D == 128 ? 3 : 6;
-  static constexpr int kWarpBytes = kStages * 2 * kHalf;
-  static constexpr int kSmemBytes = kFewWarps * kWarpBytes;
-  static_assert(kFewWarps * kFewRows * (D + 4) * 4 <= kSmemBytes, "the joined results reuse the rings");
-};
-
-__device__ __forceinline__ void ldmatrix_x4(uint32_t (&r)[4], uint32_t addr) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(addr));
-}
-__device__ __forceinline__ void ldmatrix_x4_trans(uint32_t (&r)[4], uint32_t addr) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(addr));
-}
-template <bool F16>
-__device__ __forceinline__ void mma_16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  if constexpr (F16)
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-  else
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-// 16 bytes, or zeros
-__device__ __forceinline__ void cp_async16_or_zero(uint32_t dst, const void* src, bool read) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(read ? 16 : 0) : "memory");
-}
-
-template <int D, bool F16>
-__global__ void __launch_bounds__(kFewThreads, 2) rows_attn_kernel(const uint16_t* __restrict__ k_pool,
-                                                                    const uint16_t* __restrict__ v_pool,
-                                                                    const __grid_constant__ AttnParams p) {
-  using C = FewCfg<D>;
-  extern __shared__ __align__(16) unsigned char smem[];
-  __shared__ __align__(16) int32_t scratch[kFewWarps + 8];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  uint32_t* status = p.cta_status + kMaxCtas + blockIdx.x;
-  next_kernel_may_start();
-  if (threadIdx.x == 0) *status = 0;
-  Walk walk = find_run<kFewThreads>(p, p.few0, p.few1, 0, kSetupFew, scratch, 0);
-  const uint32_t ring = smem_u32(smem) + warp * C::kWarpBytes;
-  constexpr float kBias = F16 ? 7.0f : 0.0f;       // as in prefix_attn_kernel
-  constexpr int kChunks = D / 8;                   // 16-byte pieces of a row
-  constexpr int kRowsPerCopy = 32 / kChunks;       // rows that one copy of the warp covers
-  const int c_row = lane / kChunks, c_ch = lane % kChunks;
-  const int q0 = lane >> 2, kq = (lane & 3) * 2;   // fragment row (and row + 8), column pair
-  Walk::Part part;
-  while (walk.next(p, &part)) {
-    const Item& t = part.t;
-    const bool pre = t.b < 0;
-    const int L = pre ? p.P : tail_of(p, t.b);
-    const int32_t* list = pre ? p.prefix_pages : p.tail_pages + static_cast<long long>(t.b) * p.tail_width;
-    const int key0 = part.x0 * kKeys;
-    const int key1 = part.n > 0 ? min(part.x1 * kKeys, L) : key0;
-    const int groups = (key1 - key0 + kGroup - 1) / kGroup;
-    const int mine = groups > warp ? (groups - warp + kFewWarps - 1) / kFewWarps : 0;
-    // page numbers of the warp's groups, 32 at a time, one per lane
-    int ids = 0;
-    auto look_up = [&](int j) {                    // groups j .. j + 31 of the warp
-      const int key = key0 + (warp + (j + lane) * kFewWarps) * kGroup;
-      ids = -1;
-      if (j + lane < mine) {
-        const int id = __ldg(list + (key >> p.page_shift));
-        if (id < 0 || id >= p.n_pages) record_status(status, kDevBadPage);
-        else ids = id;
-      }
-    };
-    auto load = [&](int j) {                       // group j of the warp into stage j % kStages
-      if (j > 0 && (j & 31) == 0) look_up(j);
-      const int id = __shfl_sync(0xffffffffu, ids, j & 31);
-      if (j < mine) {
-        const int key = key0 + (warp + j * kFewWarps) * kGroup;
-        const long long off = static_cast<long long>(max(id, 0)) * p.Hkv * p.page * D +
-                              (static_cast<long long>(t.kvh) * p.page + (key & (p.page - 1))) * D;
-        const uint32_t st = ring + (j % C::kStages) * 2 * C::kHalf;
-#pragma unroll
-        for (int i = 0; i < kGroup / kRowsPerCopy; ++i) {
-          const int r = i * kRowsPerCopy + c_row;
-          const uint32_t dst = st + r * D * 2 + ((c_ch ^ (r & 7)) << 4);
-          // a bad page, and slots past the length, are read as zeros
-          const bool read = id >= 0 && key + r < key1;
-          const long long src = off + (read ? r * D + c_ch * 8 : 0);
-          cp_async16_or_zero(dst, k_pool + src, read);
-          cp_async16_or_zero(dst + C::kHalf, v_pool + src, read);
-        }
-      }
-      asm volatile("cp.async.commit_group;" ::: "memory");
-    };
-    look_up(0);
-    // The thread's two rows: keys they see, and their Q in A-operand registers (requested
-    // before the first keys, whose traffic would hold it up).
-    int lim[2];
-    uint32_t qf[D / 16][4];
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const int r = q0 + 8 * e;
-      const uint16_t* src = nullptr;
-      lim[e] = 0;
-      if (r < t.rows) {
-        int b = t.b, rr = t.row0 + r, g;
-        if (b < 0) b = p.div_r.div(rr, &rr);
-        const int s = p.div_g.div(rr, &g);
-        const int n = queries_of(p, b);
-        if (s < n) {
-          const int v = visible(p, tail_of(p, b), n, s);
-          lim[e] = pre ? min(v, p.P) : v - p.P;
-          src = static_cast<const uint16_t*>(p.q) + b * p.q_b + (t.kvh * p.G + g) * p.q_h + s * p.q_s + kq;
-        }
-      }
-#pragma unroll
-      for (int c = 0; c < D / 16; ++c) {
-        qf[c][e] = src != nullptr ? *reinterpret_cast<const uint32_t*>(src + c * 16) : 0u;
-        qf[c][2 + e] = src != nullptr ? *reinterpret_cast<const uint32_t*>(src + c * 16 + 8) : 0u;
-      }
-    }
-#pragma unroll
-    for (int j = 0; j < C::kStages - 1; ++j) load(j);
-    float o[D / 8][4];
-#pragma unroll
-    for (int c = 0; c < D / 8; ++c)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) o[c][i] = 0.f;
-    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
-    for (int j = 0; j < mine; ++j) {
-      asm volatile("cp.async.wait_group %0;" ::"n"(C::kStages - 2) : "memory");
-      __syncwarp();                                // every lane's copies of group j; stage j - 1 is read
-      load(j + C::kStages - 1);
-      const uint32_t st = ring + (j % C::kStages) * 2 * C::kHalf;
-      const int key = key0 + (warp + j * kFewWarps) * kGroup;
-      float sc[2][4];
-#pragma unroll
-      for (int n = 0; n < 2; ++n)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) sc[n][i] = 0.f;
-#pragma unroll
-      for (int n = 0; n < 2; ++n) {
-#pragma unroll
-        for (int c = 0; c < D / 32; ++c) {         // 32 channels: four 8 x 8 matrices
-          const int r = n * 8 + (lane & 7), ch = c * 4 + (lane >> 3);
-          uint32_t kf[4];
-          ldmatrix_x4(kf, st + r * D * 2 + ((ch ^ (r & 7)) << 4));
-          mma_16816<F16>(sc[n], qf[2 * c], kf[0], kf[1]);
-          mma_16816<F16>(sc[n], qf[2 * c + 1], kf[2], kf[3]);
-        }
-      }
-      float mx[2] = {-INFINITY, -INFINITY};
-#pragma unroll
-      for (int n = 0; n < 2; ++n)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int e = i >> 1;
-          if (key + n * 8 + kq + (i & 1) >= lim[e]) sc[n][i] = -INFINITY;
-          mx[e] = fmaxf(mx[e], sc[n][i]);
-        }
-      float factor[2] = {1.f, 1.f};
-      bool rescale = false;
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], 1));
-        mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], 2));
-        const float rm = mx[e] * p.scale_log2 - kBias;
-        if (mx[e] != -INFINITY && rm > m[e] + 8.0f) {
-          if (m[e] != -INFINITY) {
-            factor[e] = fast_exp2(m[e] - rm);
-            rescale = true;
-          }
-          m[e] = rm;
-        }
-      }
-      if (__any_sync(0xffffffffu, rescale)) {
-#pragma unroll
-        for (int c = 0; c < D / 8; ++c)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) o[c][i] *= factor[i >> 1];
-        l[0] *= factor[0];
-        l[1] *= factor[1];
-      }
-      uint32_t pf[4];
-#pragma unroll
-      for (int n = 0; n < 2; ++n)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const float neg = m[e] == -INFINITY ? 0.f : -m[e];
-          const float x = fast_exp2(fmaf(sc[n][2 * e], p.scale_log2, neg));
-          const float y = fast_exp2(fmaf(sc[n][2 * e + 1], p.scale_log2, neg));
-          l[e] += x + y;
-          pf[2 * n + e] = pack2<F16>(x, y);
-        }
-#pragma unroll
-      for (int c = 0; c < D / 16; ++c) {           // 16 channels: two tiles of 8, two halves of the keys
-        const int r = (lane & 7) + (lane & 8), ch = c * 2 + (lane >> 4);
-        uint32_t vf[4];
-        ldmatrix_x4_trans(vf, st + C::kHalf + r * D * 2 + ((ch ^ (r & 7)) << 4));
-        mma_16816<F16>(o[2 * c], pf, vf[0], vf[1]);
-        mma_16816<F16>(o[2 * c + 1], pf, vf[2], vf[3]);
-      }
-    }
-    asm volatile("cp.async.wait_all;" ::: "memory");
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      l[e] += __shfl_xor_sync(0xffffffffu, l[e], 1);
-      l[e] += __shfl_xor_sync(0xffffffffu, l[e], 2);
-    }
-    // Join the warps (the rings are free now): rows of D values, then m and l.
-    __syncthreads();
-    constexpr int kPitch = D + 4;
-    float* acc = reinterpret_cast<float*>(smem);
-    __shared__ float stat[kFewWarps][kFewRows][2];
-#pragma unroll
-    for (int c = 0; c < D / 8; ++c) {
-#pragma unroll
-      for (int e = 0; e < 2; ++e)
-        *reinterpret_cast<float2*>(acc + (warp * kFewRows + q0 + 8 * e) * kPitch + c * 8 + kq) =
-            make_float2(o[c][2 * e], o[c][2 * e + 1]);
-    }
-    if ((lane & 3) == 0) {
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        stat[warp][q0 + 8 * e][0] = m[e];
-        stat[warp][q0 + 8 * e][1] = l[e];
-      }
-    }
-    __syncthreads();
-    if (threadIdx.x == 0) {
-      if (part.x0 == 0) p.first[part.i] = blockIdx.x;
-      if (part.x1 == part.total) p.last[part.i] = blockIdx.x;
-    }
-    constexpr int kPerRow = kFewThreads / kFewRows;                 // 8 threads a row
-    const int r = threadIdx.x / kPerRow;
-    if (r < t.rows) {
-      int b = t.b, rr = t.row0 + r, g;
-      if (b < 0) b = p.div_r.div(rr, &rr);
-      const int s = p.div_g.div(rr, &g);
-      if (s < queries_of(p, b)) {
-        float top = -INFINITY, sum = 0.f, w[kFewWarps];
-#pragma unroll
-        for (int k = 0; k < kFewWarps; ++k) top = fmaxf(top, stat[k][r][0]);
-#pragma unroll
-        for (int k = 0; k < kFewWarps; ++k) {
-          const float lk = stat[k][r][1];
-          w[k] = lk == 0.f ? 0.f : exp2f(stat[k][r][0] - top);
-          sum += lk == 0.f ? 0.f : w[k] * lk;
-        }
-        const long long row = p.few_base + static_cast<long long>(part.i - p.few0 + blockIdx.x) * kFewRows + r;
-        const float inv = sum == 0.f ? 0.f : 1.f / sum;
-        if (threadIdx.x % kPerRow == 0) p.part_l[row] = sum == 0.f ? -INFINITY : top + log2f(sum);
-#pragma unroll
-        for (int i = 0; i < D / (4 * kPerRow); ++i) {
-          const int d = 4 * (threadIdx.x % kPerRow + i * kPerRow);
-          float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-          for (int k = 0; k < kFewWarps; ++k) {
-            const float4 x = *reinterpret_cast<const float4*>(acc + (k * kFewRows + r) * kPitch + d);
-            f.x += w[k] * x.x; f.y += w[k] * x.y; f.z += w[k] * x.z; f.w += w[k] * x.w;
-          }
-          *reinterpret_cast<float4*>(p.part_acc + row * D + d) = make_float4(f.x * inv, f.y * inv, f.z * inv, f.w * inv);
-        }
-      }
-    }
-    __syncthreads();
-  }
 }
 
 // Joining the parts of split items, merging the caller's part and writing the rows; the last
@@ -1292,17 +1339,15 @@ __global__ void __launch_bounds__(kFewThreads, 2) rows_attn_kernel(const uint16_
 // behind its rows' work, or before it, one block would end 3 us after the others).
 constexpr int kJoinThreads = 256;
 
-__device__ __forceinline__ void gather_status(const AttnParams& p, uint32_t* status, int ctas, int few_ctas) {
+__device__ __forceinline__ void gather_status(const AttnParams& p, uint32_t* status, int ctas) {
   __shared__ uint32_t found;
   if (threadIdx.x == 0) found = 0;
   __syncthreads();
   uint32_t w = 0;
 #pragma unroll
-  for (int c0 = 0; c0 < kMaxCtas + kRowCtas; c0 += kJoinThreads) {
-    // the words of the kernels that ran
+  for (int c0 = 0; c0 < kRowCtas; c0 += kJoinThreads) {
     const int c = c0 + static_cast<int>(threadIdx.x);
-    const bool ran = c < kMaxCtas ? p.few0 > 0 && c < ctas : p.few1 > p.few0 && c < kMaxCtas + few_ctas;
-    const uint32_t x = ran ? p.cta_status[c] : 0u;
+    const uint32_t x = c < ctas ? p.cta_status[c] : 0u;
     w = max(w, x);
   }
   for (int i = threadIdx.x; i < p.B; i += kJoinThreads) {
@@ -1325,7 +1370,7 @@ __global__ void __launch_bounds__(kJoinThreads) own_join_kernel(const __grid_con
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   wait_for_kernel_before();
   if (blockIdx.x == ctas) {
-    if (blockIdx.y == 0) gather_status(p, status, ctas, 0);
+    if (blockIdx.y == 0) gather_status(p, status, ctas);
     return;
   }
   const int i = p.cta_done[blockIdx.x];
@@ -1449,7 +1494,7 @@ __device__ __forceinline__ PartList parts_of(const AttnParams& p, int i, int fir
   PartList l;
   l.n = 0;
   const bool few = i >= p.few0 && i < p.few1;
-  if (first < 0 || last < first || last >= (few ? kRowCtas : ctas)) return l;       // only after a wait gave up
+  if (first < 0 || last < first || last >= ctas) return l;       // only after a wait gave up
   if (few) {
     l.n = last - first + 1;
     l.step = kFewRows;
@@ -1467,13 +1512,13 @@ __device__ __forceinline__ PartList parts_of(const AttnParams& p, int i, int fir
 
 template <int D, bool F16>
 __global__ void __launch_bounds__(kJoinThreads) prefix_join_kernel(const __grid_constant__ AttnParams p,
-                                                                   uint32_t* status, int ctas, int few_ctas) {
+                                                                   uint32_t* status, int ctas) {
   constexpr int kPer = D / 32;
   __shared__ float acc_s[kJoinRows][kRowWarps][D];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   wait_for_kernel_before();
   if (blockIdx.x == gridDim.x - 1) {
-    gather_status(p, status, ctas, few_ctas);
+    gather_status(p, status, ctas);
     return;
   }
   const int slot = warp / kRowWarps, sub = warp % kRowWarps;
@@ -1658,7 +1703,7 @@ nabla_status check_sizes(int64_t B, int64_t Hq, int64_t Hkv, int64_t Sq, int D) 
 // A launch that may be set up while the kernel before it in the stream still runs (that
 // kernel lets it, and the kernel itself waits where it must).
 template <typename... Params, typename... Args>
-cudaError_t launch_behind(bool behind, void (*kernel)(Params...), dim3 grid, int block, size_t smem, cudaStream_t st,
+cudaError_t launch_behind(void (*kernel)(Params...), dim3 grid, int block, size_t smem, cudaStream_t st,
                           Args... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
@@ -1669,7 +1714,7 @@ cudaError_t launch_behind(bool behind, void (*kernel)(Params...), dim3 grid, int
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &attr;
-  cfg.numAttrs = behind ? 1 : 0;
+  cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
@@ -1730,37 +1775,32 @@ nabla_status launch(const AttnParams& p, const nabla_cache& cache, uint32_t* sta
   int sms = 0;
   nabla_status rc = set_up<D, F16>(&sms);
   if (rc != NABLA_OK) return rc;
-  const int ctas = sms < kMaxCtas ? sms : kMaxCtas, few_ctas = 2 * ctas;
+  if (sms < 2) return NABLA_ERR_UNSUPPORTED;
+  const bool only_few = p.few0 == 0;
+  const int sm = sms < kMaxCtas ? sms : kMaxCtas, ctas = only_few ? 2 * sm : sm;
   AttnParams a = p;
   // Whole rounds keep the CTAs on few key heads at a time (the L2 cache holds their keys);
   // items of different lengths would make a round as long as its longest (uneven prompts:
   // 327 us in rounds, 261 in runs).
   a.whole = a.shared || a.uniform == 0 ? 0 : a.n_items / ctas;
-  // Items of one length that CTAs are left for: dealt out whole, each to CTAs of its own, unless
-  // runs cut anywhere are shorter even with the change of items that one of them then has.
-  // Every CTA needs a tile.
-  const int left = a.few0 - a.whole * ctas;
-  a.apart = a.uniform > 0 && left > 0 && left <= ctas && a.uniform >= (ctas + left - 1) / left &&
-            a.uniform / (ctas / left) <= static_cast<long long>(left) * a.uniform / ctas + kSetup;
-  CUtensorMap mk, mv;
-  if (a.few0 > 0 && (!make_map_pool(&mk, cache.k, cache) || !make_map_pool(&mv, cache.v, cache))) return NABLA_ERR_CUDA;
+  const uint16_t* k = static_cast<const uint16_t*>(cache.k);
+  const uint16_t* v = static_cast<const uint16_t*>(cache.v);
   cudaError_t e;
-  if (a.few1 > a.few0) {
-    rows_attn_kernel<D, F16><<<few_ctas, kFewThreads, FewCfg<D>::kSmemBytes, st>>>(
-        static_cast<const uint16_t*>(cache.k), static_cast<const uint16_t*>(cache.v), a);
-    e = cudaGetLastError();
-    if (e != cudaSuccess) return cuda_status(e);
+  if (only_few) {
+    rows_attn_kernel<D, F16><<<ctas, kFewThreads, FewCfg<D>::kSmemBytes, st>>>(k, v, a);
+  } else {
+    CUtensorMap mk, mv;
+    if (!make_map_pool(&mk, cache.k, cache) || !make_map_pool(&mv, cache.v, cache)) return NABLA_ERR_CUDA;
+    prefix_attn_kernel<D, F16><<<ctas, kThreads, C::kSmemBytes, st>>>(mk, mv, k, v, a);
   }
-  if (a.few0 > 0) {
-    e = launch_behind(a.few1 > a.few0, prefix_attn_kernel<D, F16>, dim3(ctas), kThreads, C::kSmemBytes, st, mk, mv, a);
-    if (e != cudaSuccess) return cuda_status(e);
-  }
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return cuda_status(e);
   if (a.shared) {
     const long long blocks = (static_cast<long long>(a.Hkv) * a.B * a.R + kJoinRows - 1) / kJoinRows;
-    e = launch_behind(true, prefix_join_kernel<D, F16>, dim3(static_cast<unsigned>(blocks < 1 << 20 ? blocks : 1 << 20) + 1),
-                      kJoinThreads, 0, st, a, status, ctas, few_ctas);
+    e = launch_behind(prefix_join_kernel<D, F16>, dim3(static_cast<unsigned>(blocks < 1 << 20 ? blocks : 1 << 20) + 1),
+                      kJoinThreads, 0, st, a, status, ctas);
   } else {
-    e = launch_behind(true, own_join_kernel<D, F16>, dim3(ctas + 1, kOwnJoinBlocks), kJoinThreads, 0, st, a, status, ctas);
+    e = launch_behind(own_join_kernel<D, F16>, dim3(ctas + 1, kOwnJoinBlocks), kJoinThreads, 0, st, a, status, ctas);
   }
   return cuda_status(e);
 }
