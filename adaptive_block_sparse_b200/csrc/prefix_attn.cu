@@ -14,11 +14,12 @@
 //   * shared mode (fewer rows): the rows of ALL sequences are tiled together for the
 //     prefix, so its keys and values leave HBM once for the batch; each sequence's tail is
 //     one more item, and every result is a part that the join kernel joins.
-// Items of at most 16 rows (single tokens of a group of heads) go to rows_attn_kernel, whose
-// warps stream keys on their own; all others to prefix_attn_kernel, described next.
+// Items of at most 16 rows (single tokens of a group of heads) are walked by few_rows(), whose
+// warps stream keys on their own; the others as described next.
 // The unit of scheduling is one key tile.  A CTA (one per SM) first takes whole items, one
-// per round while all CTAs have one (own mode); what is left over is cut into equal runs of
-// units, wherever they fall inside items, so no SM waits for a long item.  Item lengths
+// per round while all CTAs have one (own mode, items of one length); what is left over is cut
+// into runs of equal length, so no SM waits for a long item: runs wherever they fall inside
+// items, or, with items of one length, items dealt out to CTAs of their own.  Item lengths
 // follow from the device's tail lengths: every CTA sums the units and finds its run
 // itself, so a captured launch follows the lengths of its replay.
 //
@@ -223,16 +224,21 @@ struct Walk {
 
 // Items [i0, i1) are cut into runs of equal length, one per CTA of those that share them.  The
 // units before a thread's items and in them, by a block-wide scan of the items' lengths.
-// `scratch`: 16-byte aligned shared memory of kBlock / 32 + 4 words; all threads call it.
+// `scratch`: kBlock / 32 + 8 words of shared memory; all threads call it.
 constexpr int kSetup = 4, kSetupFew = 2;
+// Where long items and items of few rows share the CTAs, a tile of the former counts twice: its
+// MMAs and exponentials take a CTA longer (factors 1.75, 2, 2.5: 8 sequences of 4 tokens over
+// 16384 and 4000 of their own 50, 45, 53 us; 64 tokens over 4096 and 500 46, 43, 40.5; 32
+// tokens over 32768 59.8, 59.8, 63.4).
+constexpr float kLongWeight = 2.0f;
 struct Units {
   int a, b, at, sum, total;
 };
 template <int kBlock>
 __device__ __forceinline__ Units scan_units(const AttnParams& p, int i0, int i1, int setup, int32_t* scratch) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  int32_t* sums = scratch + 4;
-  if (threadIdx.x == 0) scratch[0] = scratch[1] = scratch[2] = 0;
+  int32_t* sums = scratch + 8;
+  if (threadIdx.x < 8) scratch[threadIdx.x] = 0;
   const int n = i1 - i0, per = (n + kBlock - 1) / kBlock;
   Units u;
   u.a = min(static_cast<int>(threadIdx.x) * per, n);
@@ -263,9 +269,10 @@ __device__ __forceinline__ int run_of(int total, int c, int n, int* u0) {
   return q + (c < more ? 1 : 0);
 }
 
-// The thread whose items hold the run's start finds it (all threads call).
+// The thread whose items hold the run's start finds it (all threads call; `out`: four words of
+// the scan's scratch).
 __device__ __forceinline__ Walk find_run(const AttnParams& p, const Units& u, int i0, int c, int n, int setup,
-                                         int32_t* scratch) {
+                                         int32_t* out) {
   int u0;
   const int mine = run_of(u.total, c, n, &u0);
   if (mine > 0 && u0 >= u.at && u0 < u.at + u.sum) {
@@ -275,17 +282,17 @@ __device__ __forceinline__ Walk find_run(const AttnParams& p, const Units& u, in
       if (u0 < at + len) break;
       at += len;
     }
-    scratch[0] = i0 + i;
-    scratch[1] = u0 - at;
-    scratch[2] = mine;
+    out[0] = i0 + i;
+    out[1] = u0 - at;
+    out[2] = mine;
   }
   __syncthreads();
   Walk w;
   w.round = 1 << 30;
   w.setup = setup;
-  w.item = scratch[0];
-  w.x0 = scratch[1];
-  w.left = scratch[2];
+  w.item = out[0];
+  w.x0 = out[1];
+  w.left = out[2];
   return w;
 }
 
@@ -324,7 +331,7 @@ struct Bars {
   uint64_t o_done[2], o_free[2];    // the part's last P V landed / the accumulator was read
   uint64_t drain;
   uint32_t tmem;
-  alignas(16) int32_t scratch[kThreads / 32 + 4];
+  int32_t scratch[kThreads / 32 + 8];
   float stat[8][16][2];             // few_rows()
 };
 
@@ -419,18 +426,20 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
 // ------------------------------------------------------------------------------------
 // Items of at most 16 rows.  Bound by the cache's bytes, and by latency when those are few:
 // a 128-row MMA tile would be mostly padding and its pipeline (8 us from launch to result)
-// longer than the work.  The warps of a CTA take a run of units as above; each of kWarps warps
-// streams every kWarps-th group of 16 keys through its own ring in shared memory (cp.async, 24
-// KB in flight a warp, 192 KB an SM), multiplies with m16n8k16 MMAs (the rows as M, so the
-// scores' registers are the second product's A operand), and keeps m, l and O in registers.
-// The warps' results are joined through shared memory at the part's end.
+// longer than the work.  Four warps take a run of units as above; each streams every fourth
+// group of 16 keys through its own ring in shared memory (cp.async, 24 KB in flight a warp, 192
+// KB an SM), multiplies with m16n8k16 MMAs (the rows as M, so the scores' registers are the
+// second product's A operand), and keeps m, l and O in registers.  The warps' results are
+// joined through shared memory at the part's end.
 //
-// A call with such items only runs rows_attn_kernel (two CTAs of four warps an SM); one with a
-// long prefix for many rows as well gives them some of the CTAs of prefix_attn_kernel, whose
-// softmax warps do the same: one kernel fills the GPU, where two in turn each ramped up and
-// ran out (32 tokens over 32768: @@ us, 63.6 us in turn).
+// A call with such items only runs rows_attn_kernel (two runs an SM).  One with a prefix tiled
+// for many rows as well gives them some of the CTAs of prefix_attn_kernel, each of whose softmax
+// warpgroups does the same: one kernel fills the GPU, where two in turn each ramped up and ran
+// out (32 tokens over 32768: 60 us, 63.6 in turn; 12 sequences of 5 drafted tokens over 4099:
+// 25 us, 28 in turn).
 // ------------------------------------------------------------------------------------
 constexpr int kFewThreads = 128;
+constexpr int kFewWarps = kFewThreads / 32;
 constexpr int kGroup = 16;                 // keys of a ring stage
 
 template <int D>
@@ -468,14 +477,15 @@ __device__ __forceinline__ void cp_async16_or_zero(uint32_t dst, const void* src
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(read ? 16 : 0) : "memory");
 }
 
-// The CTA's parts.  Barrier kBar is the calling warps'; `warp` counts among them.
-template <int D, bool F16, int kWarps, int kBar>
-__device__ __forceinline__ void few_rows(const AttnParams& p, Walk walk, int cta, const uint16_t* __restrict__ k_pool,
+// A run's parts by four warps (`warp`: 0 .. 3), which share barrier `bar`.
+template <int D, bool F16>
+__device__ __forceinline__ void few_rows(const AttnParams& p, Walk walk, int run, const uint16_t* __restrict__ k_pool,
                                          const uint16_t* __restrict__ v_pool, unsigned char* smem,
-                                         float (*stat)[kFewRows][2], int warp, uint32_t* status) {
+                                         float (*stat)[kFewRows][2], int warp, int bar, uint32_t* status) {
   using C = FewCfg<D>;
   const int lane = threadIdx.x & 31;
-  auto sync = [] { asm volatile("barrier.cta.sync %0, %1;" ::"n"(kBar), "n"(kWarps * 32) : "memory"); };
+  constexpr int kWarps = kFewWarps;
+  auto sync = [&] { asm volatile("barrier.cta.sync %0, %1;" ::"r"(bar), "n"(kWarps * 32) : "memory"); };
   const uint32_t ring = smem_u32(smem) + warp * C::kWarpBytes;
   constexpr float kBias = F16 ? 7.0f : 0.0f;       // as in prefix_attn_kernel
   constexpr int kChunks = D / 8;                   // 16-byte pieces of a row
@@ -659,8 +669,8 @@ __device__ __forceinline__ void few_rows(const AttnParams& p, Walk walk, int cta
     }
     sync();
     if (warp == 0 && lane == 0) {
-      if (part.x0 == 0) p.first[part.i] = cta;
-      if (part.x1 == part.total) p.last[part.i] = cta;
+      if (part.x0 == 0) p.first[part.i] = run;
+      if (part.x1 == part.total) p.last[part.i] = run;
     }
     constexpr int kPerRow = 32 * kWarps / kFewRows;                 // threads a row
     const int thread = warp * 32 + lane, r = thread / kPerRow;
@@ -678,7 +688,7 @@ __device__ __forceinline__ void few_rows(const AttnParams& p, Walk walk, int cta
           w[k] = lk == 0.f ? 0.f : exp2f(stat[k][r][0] - top);
           sum += lk == 0.f ? 0.f : w[k] * lk;
         }
-        const long long row = p.few_base + static_cast<long long>(part.i - p.few0 + cta) * kFewRows + r;
+        const long long row = p.few_base + static_cast<long long>(part.i - p.few0 + run) * kFewRows + r;
         const float inv = sum == 0.f ? 0.f : 1.f / sum;
         if (thread % kPerRow == 0) p.part_l[row] = sum == 0.f ? -INFINITY : top + log2f(sum);
 #pragma unroll
@@ -703,14 +713,14 @@ __global__ void __launch_bounds__(kFewThreads, 2) rows_attn_kernel(const uint16_
                                                                     const uint16_t* __restrict__ v_pool,
                                                                     const __grid_constant__ AttnParams p) {
   extern __shared__ __align__(16) unsigned char smem[];
-  __shared__ __align__(16) int32_t scratch[kFewThreads / 32 + 4];
+  __shared__ int32_t scratch[kFewThreads / 32 + 8];
   __shared__ float stat[kFewThreads / 32][kFewRows][2];
   uint32_t* status = p.cta_status + blockIdx.x;
   next_kernel_may_start();
   if (threadIdx.x == 0) *status = 0;
   const Walk walk = find_run(p, scan_units<kFewThreads>(p, p.few0, p.few1, kSetupFew, scratch), p.few0, blockIdx.x,
                              gridDim.x, kSetupFew, scratch);
-  few_rows<D, F16, kFewThreads / 32, 0>(p, walk, blockIdx.x, k_pool, v_pool, smem, stat, threadIdx.x >> 5, status);
+  few_rows<D, F16>(p, walk, blockIdx.x, k_pool, v_pool, smem, stat, threadIdx.x >> 5, 0, status);
 }
 
 template <int D, bool F16>
@@ -759,11 +769,20 @@ __global__ void __launch_bounds__(kThreads, 1)
   int few_cta = -1;                 // its index among the CTAs of the items of few rows
   if (p.few1 > p.few0) {
     const Units u = scan_units<kThreads>(p, p.few0, p.few1, kSetupFew, B.scratch);
-    const float long_units = static_cast<float>(n_left) * (p.uniform + kSetup);
-    const int n_long = min(max(static_cast<int>(ctas * long_units / (long_units + u.total) + 0.5f), 1), ctas - 1);
+    const float long_units = kLongWeight * n_left * (p.uniform + kSetup);
+    int n_long = min(max(static_cast<int>(ctas * long_units / (long_units + u.total) + 0.5f), 1), ctas - 1);
+    if (n_long >= 2 * n_left) {        // the same number of CTAs for each item
+      n_long = (n_long + n_left / 2) / n_left * n_left;
+      if (n_long >= ctas) n_long -= n_left;
+    }
     if (c >= n_long) few_cta = c - n_long;
-    if (few_cta >= 0) walk = find_run(p, u, p.few0, few_cta, ctas - n_long, kSetupFew, B.scratch);
-    else walk = find_run_of_equals(p.uniform, i0, n_left, c, n_long);
+    if (few_cta >= 0) {                // a run for each of its two softmax warpgroups
+      const Walk w0 = find_run(p, u, p.few0, 2 * few_cta, 2 * (ctas - n_long), kSetupFew, B.scratch);
+      const Walk w1 = find_run(p, u, p.few0, 2 * few_cta + 1, 2 * (ctas - n_long), kSetupFew, B.scratch + 4);
+      walk = warp < kSoftmaxWarp0 + 4 ? w0 : w1;
+    } else {
+      walk = find_run_of_equals(p.uniform, i0, n_left, c, n_long);
+    }
   } else if (p.uniform > 0 && n_left > 0) {
     walk = find_run_of_equals(p.uniform, i0, n_left, c, ctas);
   } else {
@@ -996,7 +1015,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else {
     reg_alloc<kRegSoftmax>();
     if (few_cta >= 0) {
-      few_rows<D, F16, 8, 5>(p, walk, few_cta, k_pool, v_pool, smem, B.stat, warp - kSoftmaxWarp0, status);
+      const int half = (warp - kSoftmaxWarp0) >> 2;
+      few_rows<D, F16>(p, walk, 2 * few_cta + half, k_pool, v_pool, smem + half * FewCfg<D>::kSmemBytes,
+                       B.stat + half * kFewWarps, warp & 3, 5 + half, status);
       walk.left = 0;
     }
     // -------------------------------------------------------------------- softmax of a slot
@@ -1494,7 +1515,7 @@ __device__ __forceinline__ PartList parts_of(const AttnParams& p, int i, int fir
   PartList l;
   l.n = 0;
   const bool few = i >= p.few0 && i < p.few1;
-  if (first < 0 || last < first || last >= ctas) return l;       // only after a wait gave up
+  if (first < 0 || last < first || last >= (few ? kRowCtas : ctas)) return l;       // only after a wait gave up
   if (few) {
     l.n = last - first + 1;
     l.step = kFewRows;
@@ -1781,7 +1802,7 @@ nabla_status launch(const AttnParams& p, const nabla_cache& cache, uint32_t* sta
   AttnParams a = p;
   // Whole rounds keep the CTAs on few key heads at a time (the L2 cache holds their keys);
   // items of different lengths would make a round as long as its longest (uneven prompts:
-  // 327 us in rounds, 261 in runs).
+  // 327 us in rounds, 261 in runs at the time).
   a.whole = a.shared || a.uniform == 0 ? 0 : a.n_items / ctas;
   const uint16_t* k = static_cast<const uint16_t*>(cache.k);
   const uint16_t* v = static_cast<const uint16_t*>(cache.v);
