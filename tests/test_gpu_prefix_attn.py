@@ -149,6 +149,12 @@ CASES = {
                           q_len=[60, 1, 0, 17], dtype=F16),
     "part": dict(B=3, Hq=4, Hkv=2, D=128, Sq=7, P=200, tails=[0, 50, 300], page=64, part=F32),
     "part bf16": dict(B=2, Hq=2, Hkv=2, D=64, Sq=5, P=0, tails=[0, 20], page=16, part=BF),
+    # long and few-row items on one kernel's CTAs: fewer and more long items than CTAs, short prefixes
+    "shared CTAs": dict(B=20, Hq=60, Hkv=60, D=64, Sq=1, P=700, tails=[3 * i for i in range(20)], page=16),
+    "shared CTAs many": dict(B=20, Hq=160, Hkv=160, D=64, Sq=1, P=200, tails=[i % 9 for i in range(20)], page=16, dtype=F16),
+    "shared CTAs one tile": dict(B=18, Hq=3, Hkv=1, D=128, Sq=5, P=1, tails=[200 * (i % 3) + 5 for i in range(18)], page=32,
+                                 causal=True),
+    "shared CTAs long tail": dict(B=17, Hq=1, Hkv=1, D=128, Sq=1, P=130, tails=[0] * 16 + [20000], page=256),
     # many rows of a sequence: prefix and tail in one walk
     "chunk": dict(B=2, Hq=2, Hkv=2, D=128, Sq=300, P=1000, tails=None, page=64),
     "chunk f16": dict(B=1, Hq=3, Hkv=1, D=64, Sq=400, P=333, tails=[500], page=32, dtype=F16),
