@@ -114,6 +114,7 @@ struct AttnParams {
   int n_prefix;                     // prefix items (shared mode)
   int n_items, whole;               // whole: rounds of whole items
   int few0, few1;                   // items [few0, few1) have few rows
+  int apart;                        // rows_attn_kernel: CTAs for each item, one tile each (0: runs)
   int uniform;                      // length of every item before few0 if the host knows it
   int tail_rows;                    // rows of a tail part
   // workspace
@@ -718,9 +719,22 @@ __global__ void __launch_bounds__(kFewThreads, 2) rows_attn_kernel(const uint16_
   uint32_t* status = p.cta_status + blockIdx.x;
   next_kernel_may_start();
   if (threadIdx.x == 0) *status = 0;
-  const Walk walk = find_run(p, scan_units<kFewThreads>(p, p.few0, p.few1, kSetupFew, scratch), p.few0, blockIdx.x,
-                             gridDim.x, kSetupFew, scratch);
-  few_rows<D, F16>(p, walk, blockIdx.x, k_pool, v_pool, smem, stat, threadIdx.x >> 5, 0, status);
+  Walk walk;
+  int run = blockIdx.x;
+  if (p.apart > 0) {
+    // (every item's first tile, then the second ones: the busy CTAs are on SMs of their own)
+    const int n = p.few1 - p.few0, j = static_cast<int>(blockIdx.x) / n, i = static_cast<int>(blockIdx.x) - j * n;
+    walk.round = 1 << 30;
+    walk.setup = 0;
+    walk.item = p.few0 + i;
+    walk.x0 = j;
+    walk.left = j < p.apart && j < length_of(item_of(p, walk.item)) ? 1 : 0;
+    run = i * p.apart + j;
+  } else {
+    walk = find_run(p, scan_units<kFewThreads>(p, p.few0, p.few1, kSetupFew, scratch), p.few0, blockIdx.x, gridDim.x,
+                    kSetupFew, scratch);
+  }
+  few_rows<D, F16>(p, walk, run, k_pool, v_pool, smem, stat, threadIdx.x >> 5, 0, status);
 }
 
 template <int D, bool F16>
@@ -1808,6 +1822,10 @@ nabla_status launch(const AttnParams& p, const nabla_cache& cache, uint32_t* sta
   const uint16_t* v = static_cast<const uint16_t*>(cache.v);
   cudaError_t e;
   if (only_few) {
+    // A small call has a CTA for every tile that its page tables can hold: no scan of the lengths
+    // (32 sequences' tails of up to 100 tokens, 8 heads: 11.4 us after 12.4).
+    const int per = ctas / a.n_items, most = a.P > a.tail_width * a.page ? a.P : a.tail_width * a.page;
+    a.apart = (most + kKeys - 1) / kKeys <= per ? per : 0;
     rows_attn_kernel<D, F16><<<ctas, kFewThreads, FewCfg<D>::kSmemBytes, st>>>(k, v, a);
   } else {
     CUtensorMap mk, mv;

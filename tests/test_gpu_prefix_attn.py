@@ -149,6 +149,9 @@ CASES = {
                           q_len=[60, 1, 0, 17], dtype=F16),
     "part": dict(B=3, Hq=4, Hkv=2, D=128, Sq=7, P=200, tails=[0, 50, 300], page=64, part=F32),
     "part bf16": dict(B=2, Hq=2, Hkv=2, D=64, Sq=5, P=0, tails=[0, 20], page=16, part=BF),
+    # few-row items alone, more tiles than CTAs
+    "many tails": dict(B=40, Hq=16, Hkv=8, D=64, Sq=1, P=0, tails=[(11 * i) % 301 for i in range(40)], page=16),
+    "long and short tail": dict(B=2, Hq=4, Hkv=2, D=128, Sq=2, P=77, tails=[15000, 5], page=64, causal=True, dtype=F16),
     # long and few-row items on one kernel's CTAs: fewer and more long items than CTAs, short prefixes
     "shared CTAs": dict(B=20, Hq=60, Hkv=60, D=64, Sq=1, P=700, tails=[3 * i for i in range(20)], page=16),
     "shared CTAs many": dict(B=20, Hq=160, Hkv=160, D=64, Sq=1, P=200, tails=[i % 9 for i in range(20)], page=16, dtype=F16),
