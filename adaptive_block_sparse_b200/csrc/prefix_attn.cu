@@ -34,6 +34,13 @@
 //
 // Rows of V past a length are zeroed in shared memory (a cache slot there may hold NaN, and
 // 0 * NaN would reach O); scores past a length are replaced by -inf.
+//
+// Long items are bound by the tensor pipe and the softmax's issue slots between two MMAs of a
+// slot (a tile of 256 rows: 2.1 us, 1.8 with the MMAs alone): 2 x 7,168 tokens over 14,336 keys,
+// 24 heads, D = 128: 2.15 ms, 1.18 PF/s.  A prefix shared by single tokens is bound by HBM:
+// 32 tokens over 32768 keys and tails up to 1500, 227 MB: 60 us, of which the bytes take 38.
+// Half as large score tiles, a second issuer, four softmax warpgroups, five stages, and masked
+// tiles on the one-pass path (more registers) were all slower.
 #include <math.h>
 
 #include <atomic>
@@ -437,7 +444,8 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
 // for many rows as well gives them some of the CTAs of prefix_attn_kernel, each of whose softmax
 // warpgroups does the same: one kernel fills the GPU, where two in turn each ramped up and ran
 // out (32 tokens over 32768: 60 us, 63.6 in turn; 12 sequences of 5 drafted tokens over 4099:
-// 25 us, 28 in turn).
+// 25 us, 28 in turn).  Alone: 4 tokens over 1000 + 150 keys 10.4 us, join included (latency);
+// 32 tokens over tails up to 1500, 98 MB: 30 us.
 // ------------------------------------------------------------------------------------
 constexpr int kFewThreads = 128;
 constexpr int kFewWarps = kFewThreads / 32;
@@ -1396,7 +1404,8 @@ __device__ __forceinline__ void gather_status(const AttnParams& p, uint32_t* sta
 
 // Own mode: many rows with few parts each.  A warp joins eight rows at a time, four lanes a
 // row for the log-sums (four parts at a time), then all lanes for a row's channels.  Bound by
-// the latency of its loads.
+// the latency of its loads: 12 tiles in 12 parts each 15 us with cold caches (four rows a warp
+// and four parts in flight: no faster).
 constexpr int kOwnJoinBlocks = kRows / 64;
 template <int D, bool F16>
 __global__ void __launch_bounds__(kJoinThreads) own_join_kernel(const __grid_constant__ AttnParams p, uint32_t* status,
@@ -1510,7 +1519,8 @@ __global__ void __launch_bounds__(kJoinThreads) own_join_kernel(const __grid_con
   }
 }
 
-// Shared mode.  Four warps share a row: a long prefix leaves a row a part in every CTA, and
+// Shared mode.  Bound by latency (about 4 us: first and last CTA, log-sums, accumulators).
+// Four warps share a row: a long prefix leaves a row a part in every CTA, and
 // they are read in parallel (every fourth part by one warp, always the same ones, so results
 // do not depend on timing).
 constexpr int kRowWarps = 4;
