@@ -400,9 +400,9 @@ nabla_status nabla_cache_append(nabla_heads k, nabla_heads v, nabla_heads q_src,
                                 const nabla_rope *rope, nabla_grid frame, int64_t pos0,
                                 const int32_t *positions, uint32_t *status, nabla_stream_t stream);
 
-/* Attention (forward only) of B sequences over a prefix that all of them share and over each sequence's own
- * tail, both in the paged cache.  With few query rows per sequence the rows of all sequences
- * walk the prefix together, so its keys and values are read once for the batch.
+/* Attention (forward only) of B sequences over a prefix that all of them share and over each
+ * sequence's own tail, both in the paged cache.  With few query rows per sequence the rows of
+ * all sequences walk the prefix together, so its keys and values are read once for the batch.
  *   s_ij = scale * q_i . k_j over the visible keys j (prefix first, then the tail),
  *   O_i = sum_j softmax_j(s_ij) v_j,  LSE_i = ln sum_j exp(s_ij);  no visible key: O = 0,
  *   LSE = -inf.
