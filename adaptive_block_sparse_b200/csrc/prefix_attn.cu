@@ -9,8 +9,8 @@
 // Work.  An item is a tile of up to 256 query rows of one key head and a run of 128-key
 // tiles.  The heads that share a key head are rows too (row = query * G + head in group), so
 // a key tile is read once for all of them.
-//   * own mode (a sequence has at least 256 rows per key head): an item is 256 rows of one
-//     sequence and walks the prefix, then the sequence's tail;
+//   * own mode (a sequence has at least 256 rows per key head, or 128 and a short prefix): an
+//     item is up to 256 rows of one sequence and walks the prefix, then the sequence's tail;
 //   * shared mode (fewer rows): the rows of ALL sequences are tiled together for the
 //     prefix, so its keys and values leave HBM once for the batch; each sequence's tail is
 //     one more item, and every result is a part that the join kernel joins.
@@ -1520,11 +1520,12 @@ __global__ void __launch_bounds__(kJoinThreads) own_join_kernel(const __grid_con
 }
 
 // Shared mode.  Bound by latency (about 4 us: first and last CTA, log-sums, accumulators).
-// Four warps share a row: a long prefix leaves a row a part in every CTA, and
-// they are read in parallel (every fourth part by one warp, always the same ones, so results
-// do not depend on timing).
-constexpr int kRowWarps = 4;
-constexpr int kJoinRows = kJoinThreads / 32 / kRowWarps;     // rows at a time
+// Four warps share a row: a long prefix leaves a row a part in every CTA, and they are read in
+// parallel (every fourth part by one warp, always the same ones, so results do not depend on
+// timing).  With more rows than are resident that way a warp has a row to itself (a call with
+// 52,080 rows in two parts: 74 us, 147 with four warps each).
+constexpr int kJoinWarps = kJoinThreads / 32;
+constexpr int kFewJoinRows = kMaxCtas * (2048 / kJoinThreads) * (kJoinWarps / 4);
 
 // Parts of one item that hold a row: the first in workspace row r0, part j > 0 in r1 +
 // (j - 1) step.
@@ -1555,11 +1556,12 @@ __device__ __forceinline__ PartList parts_of(const AttnParams& p, int i, int fir
   return l;
 }
 
-template <int D, bool F16>
+template <int D, bool F16, int kRowWarps>
 __global__ void __launch_bounds__(kJoinThreads) prefix_join_kernel(const __grid_constant__ AttnParams p,
                                                                    uint32_t* status, int ctas) {
   constexpr int kPer = D / 32;
-  __shared__ float acc_s[kJoinRows][kRowWarps][D];
+  constexpr int kJoinRows = kJoinWarps / kRowWarps;     // rows at a time
+  __shared__ float acc_s[kRowWarps > 1 ? kJoinRows : 1][kRowWarps][D];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   wait_for_kernel_before();
   if (blockIdx.x == gridDim.x - 1) {
@@ -1630,16 +1632,20 @@ __global__ void __launch_bounds__(kJoinThreads) prefix_join_kernel(const __grid_
         }
       }
     }
+    if constexpr (kRowWarps > 1) {
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) acc_s[slot][sub][lane * kPer + i] = acc[i];
-    __syncthreads();
+      for (int i = 0; i < kPer; ++i) acc_s[slot][sub][lane * kPer + i] = acc[i];
+      __syncthreads();
+    }
     if (live && sub == 0) {
+      if constexpr (kRowWarps > 1) {
 #pragma unroll
-      for (int i = 0; i < kPer; ++i) {
-        float x = 0.f;
+        for (int i = 0; i < kPer; ++i) {
+          float x = 0.f;
 #pragma unroll
-        for (int k = 0; k < kRowWarps; ++k) x += acc_s[slot][k][lane * kPer + i];
-        acc[i] = x;
+          for (int k = 0; k < kRowWarps; ++k) x += acc_s[slot][k][lane * kPer + i];
+          acc[i] = x;
+        }
       }
       float lse2 = m == -INFINITY ? -INFINITY : m + log2f(sum);
       if (nan) lse2 = __int_as_float(0x7FC00000);
@@ -1674,7 +1680,7 @@ __global__ void __launch_bounds__(kJoinThreads) prefix_join_kernel(const __grid_
         else *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.o) + off + i) = pack2<F16>(acc[i], acc[i + 1]);
       }
     }
-    __syncthreads();
+    if constexpr (kRowWarps > 1) __syncthreads();
   }
 }
 
@@ -1695,6 +1701,16 @@ bool make_map_pool(CUtensorMap* map, const void* base, const nabla_cache& c) {
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Shared mode, for R rows per sequence and key head and a prefix of P tokens.  From 128 rows on a
+// sequence fills at least half of an item by itself: over a short prefix the padding of its
+// 256 rows costs less than parts and their join.  Own against shared, us: 130 rows over 300,
+// 1000, 3000 tokens 38 : 45, 48 : 49, 73 : 66; 168 rows over 1000, 3000, 6000 79 : 109, 140 :
+// 154, 221 : 214; 200 rows over 3000, 12000 134 : 155, 367 : 374.
+bool is_shared(long long R, long long P) {
+  if (R < kRows / 2 || R >= kRows) return R < kRows;
+  return (kRows - R) * ((P + kKeys - 1) / kKeys) > 16 * R;
+}
+
 // How a call is cut into items, and its workspace.
 struct Plan {
   bool shared;
@@ -1704,10 +1720,10 @@ struct Plan {
   size_t off_first, off_last, off_l, off_acc, bytes;
 };
 
-Plan make_plan(long long B, long long Hkv, long long G, long long Sq, int D) {
+Plan make_plan(long long B, long long Hkv, long long G, long long Sq, int D, bool shared) {
   Plan a;
   const long long R = G * Sq;
-  a.shared = R < kRows;
+  a.shared = shared;
   if (a.shared) {
     a.n_rt = (B * R + kRows - 1) / kRows;
     a.n_prefix = Hkv * a.n_rt;
@@ -1845,9 +1861,13 @@ nabla_status launch(const AttnParams& p, const nabla_cache& cache, uint32_t* sta
   e = cudaGetLastError();
   if (e != cudaSuccess) return cuda_status(e);
   if (a.shared) {
-    const long long blocks = (static_cast<long long>(a.Hkv) * a.B * a.R + kJoinRows - 1) / kJoinRows;
-    e = launch_behind(prefix_join_kernel<D, F16>, dim3(static_cast<unsigned>(blocks < 1 << 20 ? blocks : 1 << 20) + 1),
-                      kJoinThreads, 0, st, a, status, ctas);
+    const long long rows = static_cast<long long>(a.Hkv) * a.B * a.R;
+    const bool few = rows <= kFewJoinRows;
+    const int at_once = few ? kJoinWarps / 4 : kJoinWarps;
+    const long long blocks = (rows + at_once - 1) / at_once;
+    e = launch_behind(few ? prefix_join_kernel<D, F16, 4> : prefix_join_kernel<D, F16, 1>,
+                      dim3(static_cast<unsigned>(blocks < 1 << 20 ? blocks : 1 << 20) + 1), kJoinThreads, 0, st, a, status,
+                      ctas);
   } else {
     e = launch_behind(own_join_kernel<D, F16>, dim3(ctas + 1, kOwnJoinBlocks), kJoinThreads, 0, st, a, status, ctas);
   }
@@ -1861,7 +1881,11 @@ using namespace nabla;
 
 extern "C" size_t nabla_prefix_workspace_bytes(int32_t B, int32_t Hq, int32_t Hkv, int32_t Sq, int32_t D) {
   if (check_sizes(B, Hq, Hkv, Sq, D) != NABLA_OK) return 0;
-  return make_plan(B, Hkv, Hq / Hkv, Sq, D).bytes;
+  const int G = Hq / Hkv;
+  const size_t shared = make_plan(B, Hkv, G, Sq, D, true).bytes, own = make_plan(B, Hkv, G, Sq, D, false).bytes;
+  const long long R = static_cast<long long>(G) * Sq;
+  if (R < kRows / 2 || R >= kRows) return R < kRows ? shared : own;
+  return shared > own ? shared : own;            // the prefix's length decides
 }
 
 extern "C" nabla_status nabla_prefix_attn(nabla_heads q, int32_t B, int32_t Sq, nabla_cache cache,
@@ -1922,7 +1946,7 @@ extern "C" nabla_status nabla_prefix_attn(nabla_heads q, int32_t B, int32_t Sq, 
       return NABLA_ERR_INVALID_ARG;
   }
   const int G = q.H / cache.H;
-  const Plan plan = make_plan(B, cache.H, G, Sq, cache.D);
+  const Plan plan = make_plan(B, cache.H, G, Sq, cache.D, is_shared(static_cast<int64_t>(G) * Sq, prefix_len));
   if (!workspace || workspace_bytes < plan.bytes || (reinterpret_cast<uintptr_t>(workspace) & 255))
     return NABLA_ERR_WORKSPACE;
   AttnParams p = {};

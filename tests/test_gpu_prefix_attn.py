@@ -149,6 +149,13 @@ CASES = {
                           q_len=[60, 1, 0, 17], dtype=F16),
     "part": dict(B=3, Hq=4, Hkv=2, D=128, Sq=7, P=200, tails=[0, 50, 300], page=64, part=F32),
     "part bf16": dict(B=2, Hq=2, Hkv=2, D=64, Sq=5, P=0, tails=[0, 20], page=16, part=BF),
+    "more rows than join blocks": dict(B=31, Hq=16, Hkv=2, D=64, Sq=21, P=33, tails=[(5 * i) % 48 for i in range(31)], page=32,
+                                       part=F32, dtype=F16, q_len=[21 - i % 3 for i in range(31)]),
+    # 128 to 255 rows a sequence: items of their own over a short prefix, parts over a long one
+    "half a tile": dict(B=3, Hq=4, Hkv=2, D=128, Sq=64, P=200, tails=[64, 300, 70], page=32, causal=True, part=F32),
+    "half a tile f16": dict(B=4, Hq=5, Hkv=1, D=64, Sq=31, P=130, tails=[0, 31, 40, 129], page=16, dtype=F16, q_len=[31, 0, 30, 31]),
+    "half a tile long": dict(B=3, Hq=4, Hkv=2, D=128, Sq=64, P=4000, tails=[64, 300, 70], page=32, causal=True, part=F32),
+    "half a tile alone": dict(B=2, Hq=3, Hkv=3, D=128, Sq=255, P=2100, tails=None, page=128),
     # few-row items alone, more tiles than CTAs
     "many tails": dict(B=40, Hq=16, Hkv=8, D=64, Sq=1, P=0, tails=[(11 * i) % 301 for i in range(40)], page=16),
     "long and short tail": dict(B=2, Hq=4, Hkv=2, D=128, Sq=2, P=77, tails=[15000, 5], page=64, causal=True, dtype=F16),
