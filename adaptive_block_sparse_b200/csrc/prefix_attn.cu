@@ -727,6 +727,7 @@ __global__ void __launch_bounds__(kFewThreads, 2) rows_attn_kernel(const uint16_
   uint32_t* status = p.cta_status + blockIdx.x;
   next_kernel_may_start();
   if (threadIdx.x == 0) *status = 0;
+  __syncthreads();         // any warp may record into the word from here on
   Walk walk;
   int run = blockIdx.x;
   if (p.apart > 0) {

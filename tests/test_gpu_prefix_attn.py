@@ -354,6 +354,31 @@ def test_bad_pages_and_lengths_are_reported():
     assert status(q_len=ints([1, -1, 1, 1]))[0] == m.DEVICE_BAD_LENGTH
 
 
+@pytest.mark.parametrize("warp", [0, 1, 2, 3])
+@pytest.mark.parametrize("name", ["token", "many tails"])
+def test_a_bad_page_of_any_warp_is_reported(name, warp):
+    """Items of few rows, a CTA a tile and in runs: a warp reads every fourth group of 16 keys, here
+    a page.  The one bad page is some warp's, the workspace holds what an earlier call left."""
+    m = nbl()
+    pr = Problem(**CASES[name], seed=16)
+    b = int(np.argmax(pr.tails))
+    assert pr.page == 16 and pr.tails[b] > 64
+    need = m.nabla_prefix_workspace_bytes(pr.B, pr.Hq, pr.Hkv, pr.Sq, pr.D)
+    base = pr.run()[0]
+    table = pr.table.copy()
+    table[b, warp] = pr.caches[0].shape[0]
+    bad = {**pr.args(), "tail_pages": ints(table)}
+    for left in (0x00, 0x5A, 0xFF) * 10:
+        ws = torch.full((need,), left, dtype=torch.uint8, device=DEV)
+        o, _ = m.nabla_prefix_attn(pr.q, *pr.caches, **bad, workspace=ws)
+        assert m.nabla_read_device_status(ws) == m.DEVICE_BAD_PAGE
+        others = [i for i in range(pr.B) if i != b]
+        assert torch.equal(o[others], base[others])
+        ws.fill_(left)
+        m.nabla_prefix_attn(pr.q, *pr.caches, **pr.args(), workspace=ws)
+        assert m.nabla_read_device_status(ws) == 0
+
+
 def test_graph_follows_the_lengths_and_side_streams():
     """A captured call replayed with other lengths, and two calls at once with workspaces of their
     own."""
