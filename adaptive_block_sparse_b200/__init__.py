@@ -484,8 +484,8 @@ def nabla_rotary(q, k, rope: Rope, grid=None, positions=None, origin=(0, 0, 0), 
 def nabla_cache_append(k, v, k_cache, v_cache, page_table, start, rope: Rope = None, frame=(1, 1), pos0=0,
                        positions=None, counts=None, q=None, q_out=None, status=None, stream=None):
     """Append ``k`` (rotated on the way when ``rope`` is given) and ``v`` [B, H, S, D] to the
-    paged cache at the sequences' tokens start[b] .. start[b] + counts[b] - 1; with ``q``,
-    rotate it in the same launch.  ``frame``: (Hg, W) of a latent frame for three axes.
+    paged cache at the sequences' tokens start[b] .. start[b] + counts[b] - 1 (0 <= counts[b] <= S,
+    None: S); with ``q``, rotate it in the same launch.  ``frame``: (Hg, W) of a latent frame for three axes.
     ``status``: uint8 or int32 CUDA tensor of at least 4 zeroed bytes for
     ``nabla_read_device_status``.  Returns q_out (None without q)."""
     if stream is not None:

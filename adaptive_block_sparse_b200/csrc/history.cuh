@@ -9,7 +9,7 @@ namespace nabla {
 // Device status codes of these operators (first error wins, as for every other call).
 enum : uint32_t {
   kDevBadPage = 0x301,     // a page number outside the cache: that page was not touched
-  kDevBadLength = 0x302,   // a negative length, or one beyond the page table
+  kDevBadLength = 0x302,   // a negative length, or one beyond the page table or the call's tokens
 };
 
 // Host checks shared by the entry points.

@@ -138,7 +138,11 @@ __device__ __forceinline__ Token locate(const RotaryParams& p, int token) {
   long long page_off = 0;
   if (p.table != nullptr) {
     const long long at = static_cast<long long>(p.start[b]) + n;
-    k.stored = p.counts == nullptr || n < p.counts[b];
+    if (p.counts != nullptr) {
+      const int c = p.counts[b];
+      k.stored = n < c;
+      if (n == 0 && (c < 0 || c > p.S)) record_status(p.status, kDevBadLength);
+    }
     if (k.stored) {
       const long long pg = at >> p.page_shift;
       int id = -1;

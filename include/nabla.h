@@ -367,8 +367,8 @@ nabla_status nabla_rotary(nabla_heads q_src, nabla_heads q_dst, nabla_heads k_sr
 /* A paged cache of keys and values: two pools [n_pages, H, page, D] of bf16 or fp16.  page:
  * tokens per page, a power of two from 16 to 4096.  A sequence is a list of page numbers; its
  * token i is slot i % page of its page i / page.  Page numbers outside [0, n_pages) are never
- * dereferenced: they are reported (0x301), as are lengths below 0 or beyond a page list
- * (0x302). */
+ * dereferenced: they are reported (0x301), as are lengths below 0, beyond a page list or, for
+ * the tokens of a call, beyond the call's (0x302). */
 typedef struct {
   void *k, *v;
   int32_t n_pages, H, page, D;
@@ -384,14 +384,15 @@ typedef struct {
  * page_table : int32 [B, table_width] page numbers; table_width * page < 2^31.
  * start      : int32 [B], index in its sequence of each sequence's first new token.
  * counts     : nullable int32 [B]: tokens to append of each sequence (the first counts[b] of
- *              its S; NULL = all S).  The others write nothing.
+ *              its S, 0 <= counts[b] <= S; NULL = all S).  The others write nothing.  One
+ *              below 0 or above S is reported (0x302) and taken as 0 or S.
  * rope       : nullable (host pointer): without it K is stored as given.  The position of a
  *              token is p = pos0 + its index in the sequence; with three axes p = (t, h, w)
  *              on frames of frame.Hg x frame.W tokens (frame.T is ignored).
  * positions  : nullable int32 [B, S, axes], replaces p.
- * status     : nullable device word that receives 0x301 / 0x302 (first one wins; the token
- *              concerned is skipped).  The call does not clear it: zero it before its
- *              first use; nabla_read_device_status reads and clears it.
+ * status     : nullable device word that receives 0x301 / 0x302 (first one wins; a token
+ *              without a place in the cache is skipped).  The call does not clear it: zero
+ *              it before its first use; nabla_read_device_status reads and clears it.
  * Two tokens of one call must not land in the same slot.  Errors: INVALID_ARG, UNSUPPORTED,
  * CUDA. */
 nabla_status nabla_cache_append(nabla_heads k, nabla_heads v, nabla_heads q_src, nabla_heads q_dst,

@@ -267,6 +267,42 @@ def test_cache_append_skips_bad_pages_and_lengths():
     assert torch.equal(vc[4], v[2, :, :16]) and torch.equal(vc[5, :, :4], v[2, :, 16:])
 
 
+@pytest.mark.parametrize("with_q", [False, True])
+@pytest.mark.parametrize("dim", [64, 10])
+def test_cache_append_reports_counts_outside_the_batch(dim, with_q):
+    """counts below 0 or beyond S: reported, the former appends nothing and the latter S tokens."""
+    m = nbl()
+    B, S, Hkv, Hq, D, page = 4, 20, 2, 3, 64, 16
+    rope = m.Rope.build(dim, DEV, m.NABLA_ROPE_HALF)         # 10: turned in shared memory
+    k, v, q = (rnd((B, h, S, D), torch.bfloat16, i) for i, h in enumerate((Hkv, Hkv, Hq)))
+    q = q if with_q else None
+    table = torch.arange(12, dtype=torch.int32, device=DEV).reshape(B, 3)
+    start = torch.tensor([3, 0, 5, 28], dtype=torch.int32, device=DEV)
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+
+    def append(counts, word=status):
+        pools = [torch.full((12, Hkv, page, D), 9.0, dtype=torch.bfloat16, device=DEV) for _ in range(2)]
+        n = None if counts is None else torch.tensor(counts, dtype=torch.int32, device=DEV)
+        qo = m.nabla_cache_append(k, v, *pools, table, start, rope=rope, counts=n, q=q, status=word)
+        return pools, qo
+    want, wq = append([7, 0, S, S])
+    assert m.nabla_read_device_status(status) == 0
+    for counts in ([7, -1, S, S], [7, 0, S + 1, S], [7, 0, S, 1 << 30], [7, -(1 << 31), (1 << 31) - 1, S]):
+        got, gq = append(counts)
+        assert m.nabla_read_device_status(status) == m.DEVICE_BAD_LENGTH, counts
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+        assert gq is None if q is None else torch.equal(gq, wq)
+        assert all(torch.equal(a, b) for a, b in zip(append(counts, None)[0], want))     # without a word
+    assert m.nabla_read_device_status(status) == 0
+    # an earlier error stays: the first one wins
+    append([7, S + 1, S, S])
+    table[0, 0] = 12
+    append([7, 0, S, S])
+    assert m.nabla_read_device_status(status) == m.DEVICE_BAD_LENGTH
+    append([0, -5, 0, 0])
+    assert m.nabla_read_device_status(status) == m.DEVICE_BAD_LENGTH
+
+
 def test_binding_refuses():
     """What the C side cannot see; nothing is launched."""
     m = nbl()
