@@ -998,7 +998,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       // ------------------------------------------------------------------ Q rows
       // Two warps gather the tile's rows into the K-major 128-byte-swizzled layout, each every
       // other 32 rows: a lane finds one row, then the warp copies the rows, D / 8 lanes a row.
-      // Rows that do not exist are zeros.
+      // Rows that do not exist, or lie behind their sequence's queries, are zeros: what a padded
+      // batch holds there (NaN, say) would fail the sum check of the whole warp in every tile
+      // (5 uneven causal prompts, NaN behind them: 379 us, 266 as zeros, with a cold L2).
       constexpr int kChunks = D / 8;
       constexpr int kStep = 32 / kChunks;
       const int c = lane % kChunks;
@@ -1017,7 +1019,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             int b = part.t.b, rr = part.t.row0 + r0 + lane, g;
             if (b < 0) b = p.div_r.div(rr, &rr);
             const int s = p.div_g.div(rr, &g);
-            off = b * p.q_b + (part.t.kvh * p.G + g) * p.q_h + s * p.q_s;
+            if (s < queries_of(p, b)) off = b * p.q_b + (part.t.kvh * p.G + g) * p.q_h + s * p.q_s;
           }
 #pragma unroll 4
           for (int i = 0; i < 32; i += kStep) {

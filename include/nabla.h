@@ -414,7 +414,7 @@ nabla_status nabla_cache_append(nabla_heads k, nabla_heads v, nabla_heads q_src,
  * tail_pages : nullable int32 [B, tail_width]; tail_len: int32 [B] on the device, required with
  *              it.  tail_width * page < 2^31.  Table entries past a tail's last page are not read.
  * q_len      : nullable int32 [B] on the device: queries of each sequence (the first q_len[b]
- *              of Sq; NULL = all).  Rows behind them are neither computed nor written.
+ *              of Sq; NULL = all).  Rows behind them are neither read nor written.
  * causal     : 0: a query sees its sequence's prefix and whole tail.  1: the queries are the
  *              sequence's last tokens: query i of q_len[b] sees the keys j <= prefix_len +
  *              tail_len[b] - q_len[b] + i.

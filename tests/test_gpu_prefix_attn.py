@@ -274,6 +274,32 @@ def test_keys_that_no_query_sees_may_hold_anything(Sq):
     assert torch.isnan(o[:, :, -1]).all() and torch.isnan(l[:, :, -1]).all()
 
 
+PADDED = {
+    "few rows": dict(B=3, Hq=4, Hkv=2, D=64, Sq=5, P=300, tails=[5, 140, 9], page=16, q_len=[5, 1, 0], causal=True),
+    "batch of rows": dict(B=6, Hq=6, Hkv=2, D=128, Sq=11, P=700, tails=None, page=32, q_len=[11, 5, 0, 11, 3, 1]),
+    "alternate slots": dict(B=2, Hq=2, Hkv=2, D=64, Sq=70, P=900, tails=[300, 333], page=32, q_len=[70, 33], dtype=F16),
+    "dual tails": dict(B=3, Hq=10, Hkv=2, D=128, Sq=40, P=300, tails=[400, 0, 300], page=64, q_len=[40, 0, 21]),
+    "chunk": dict(B=2, Hq=2, Hkv=2, D=128, Sq=500, P=1000, tails=[300, 0], page=64, q_len=[500, 277]),
+    "chunk causal": dict(B=3, Hq=2, Hkv=2, D=64, Sq=600, P=520, tails=[600, 45, 0], page=16, causal=True,
+                         q_len=[511, 45, 0], dtype=F16),
+}
+
+
+@pytest.mark.parametrize("name", list(PADDED))
+@pytest.mark.parametrize("fill", [math.nan, -math.inf, 3e4])
+def test_queries_behind_a_sequences_own_may_hold_anything(name, fill):
+    """The same bits whatever a padded batch holds behind q_len, and those rows are left alone."""
+    pr = Problem(**PADDED[name], seed=17)
+    for b, n in enumerate(pr.q_len):
+        pr.q[b, :, n:] = 0.0
+    base, bl = pr.run()
+    pr.check(base, bl)
+    for b, n in enumerate(pr.q_len):
+        pr.q[b, :, n:] = fill
+    o, l = pr.run()
+    assert torch.equal(o, base) and torch.equal(l, bl)
+
+
 @pytest.mark.parametrize("name", ["dual tails", "chunk", "chunk causal"])
 def test_bad_pages_leave_the_other_sequences_alone(name):
     m = nbl()
