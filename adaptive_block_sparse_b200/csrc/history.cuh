@@ -3,10 +3,12 @@
 #pragma once
 
 #include "common.cuh"
+#include "device_status.h"
 
 namespace nabla {
 
-// Device status codes of these operators (first error wins, as for every other call).
+// Device status codes of these operators.  Append: first error wins, as for every other call;
+// prefix attention: the largest rank of device_status.h is reported.
 enum : uint32_t {
   kDevBadPage = 0x301,     // a page number outside the cache: that page was not touched
   kDevBadLength = 0x302,   // a negative length, or one beyond the page table or the call's tokens

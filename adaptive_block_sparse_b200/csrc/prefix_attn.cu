@@ -125,7 +125,7 @@ struct AttnParams {
   int uniform;                      // length of every item before few0 if the host knows it
   int tail_rows;                    // rows of a tail part
   // workspace
-  uint32_t* cta_status;
+  uint32_t* cta_status;             // ranks of device status codes
   int32_t* cta_done;                // own mode: the split item that CTA c completes, or -1
   int32_t* first;                   // first / last CTA of an item (relative to whole * grid)
   int32_t* last;
@@ -357,6 +357,12 @@ struct Cfg {
   static __device__ __forceinline__ uint32_t col_o(int s) { return 256u + s * 128u; }
 };
 
+// A CTA's status word holds the largest rank of what its threads recorded.  (The reduction
+// itself: with atomicMax() ptxas loads 64 bytes more of spills in the long items' kernel.)
+__device__ __forceinline__ void record_rank(uint32_t* status, uint32_t code) {
+  asm volatile("red.global.max.u32 [%0], %1;" ::"l"(__cvta_generic_to_global(status)), "r"(status_rank(code)) : "memory");
+}
+
 // mbar_wait() for short hand-overs: probes without reading the timer, which is looked at (and
 // the limit applied) every 256 probes only.
 __device__ __forceinline__ bool bar_wait(uint64_t* bar, uint32_t parity, uint32_t* status, uint32_t code) {
@@ -366,11 +372,11 @@ __device__ __forceinline__ bool bar_wait(uint64_t* bar, uint32_t parity, uint32_
       const uint64_t t = global_timer_ns();
       if (t0 == 0) t0 = t;
       if (t - t0 > kWaitLimitNs) {
-        record_status(status, code);
+        record_rank(status, code);
         return false;
       }
-      // another wait of the CTA gave up (a bad page or length ends none)
-      if (*reinterpret_cast<volatile uint32_t*>(status) >> 8 == kDevTimeoutTmaFull >> 8) return false;
+      // another wait of the CTA gave up (a bad page ends none)
+      if (is_timeout_rank(*reinterpret_cast<volatile uint32_t*>(status))) return false;
     }
   }
   return true;
@@ -518,7 +524,7 @@ __device__ __forceinline__ void few_rows(const AttnParams& p, Walk walk, int run
       ids = -1;
       if (j + lane < mine) {
         const int id = __ldg(list + (key >> p.page_shift));
-        if (id < 0 || id >= p.n_pages) record_status(status, kDevBadPage);
+        if (id < 0 || id >= p.n_pages) record_rank(status, kDevBadPage);
         else ids = id;
       }
     };
@@ -866,7 +872,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int32_t* list = pre ? p.prefix_pages : p.tail_pages + static_cast<long long>(part.t.b) * p.tail_width;
           const int id = __ldg(list + (base >> p.page_shift));
           if (id < 0 || id >= p.n_pages) {
-            record_status(status, kDevBadPage);
+            record_rank(status, kDevBadPage);
             return p.n_pages;                            // out of bounds: the copy fills zeros
           }
           return id;
@@ -1397,12 +1403,12 @@ __device__ __forceinline__ void gather_status(const AttnParams& p, uint32_t* sta
     w = max(w, x);
   }
   for (int i = threadIdx.x; i < p.B; i += kJoinThreads) {
-    if (p.q_len != nullptr && queries_of(p, i) != p.q_len[i]) w = max(w, static_cast<uint32_t>(kDevBadLength));
-    if (p.tail_pages != nullptr && tail_of(p, i) != p.tail_len[i]) w = max(w, static_cast<uint32_t>(kDevBadLength));
+    if (p.q_len != nullptr && queries_of(p, i) != p.q_len[i]) w = max(w, status_rank(kDevBadLength));
+    if (p.tail_pages != nullptr && tail_of(p, i) != p.tail_len[i]) w = max(w, status_rank(kDevBadLength));
   }
   if (w != 0) atomicMax(&found, w);
   __syncthreads();
-  if (threadIdx.x == 0) *status = found;
+  if (threadIdx.x == 0) *status = status_of_rank(found);
 }
 
 // Own mode: many rows with few parts each.  A warp joins eight rows at a time, four lanes a

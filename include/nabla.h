@@ -433,8 +433,8 @@ nabla_status nabla_cache_append(nabla_heads k, nabla_heads v, nabla_heads q_src,
  * probabilities enter the second product in the cache's 16-bit type; sums and statistics are
  * f32.  Deterministic: no atomics on data.
  * workspace  : >= nabla_prefix_workspace_bytes(B, Hq, cache.H, Sq, D) bytes, 256-byte
- *              aligned; word 0 receives the device status (0x1xx, 0x301, 0x302; the rows of the
- *              sequences concerned are unspecified).
+ *              aligned; word 0 receives the device status.  0x301, 0x302: the rows of the
+ *              sequences concerned are unspecified; 0x1xx, reported before those: any row is.
  * Errors: INVALID_ARG, UNSUPPORTED, WORKSPACE, CUDA. */
 size_t nabla_prefix_workspace_bytes(int32_t B, int32_t Hq, int32_t Hkv, int32_t Sq, int32_t D);
 nabla_status nabla_prefix_attn(nabla_heads q, int32_t B, int32_t Sq, nabla_cache cache,
