@@ -101,26 +101,27 @@ def _link_binding(obj: str, verbose: bool) -> None:
     os.replace(tmp, BINDING)
 
 
+def _link(objs, verbose: bool, extra) -> None:
+    if (os.path.exists(LIB) and not extra and
+            os.path.getmtime(LIB) >= max(os.path.getmtime(o) for o in objs)):
+        return
+    tmp = LIB + ".tmp"
+    _run([nvcc(), *ARCH, "-shared", "-cudart", "static", "-o", tmp, *objs, "-lrt", "-ldl", "-lpthread"],
+         "linking the library", verbose)
+    os.replace(tmp, LIB)
+
+
 def build(verbose: bool = False, extra=()) -> str:
     """Compile every CUDA source, link ``libnabla.so`` and build ``_binding.so``; returns the
-    library's path."""
+    library's path.  The library is there even if the binding cannot be built (a C program needs
+    neither it nor torch's headers); that is raised afterwards."""
     os.makedirs(BUILD, exist_ok=True)
     srcs = _sources()
     with cf.ThreadPoolExecutor(max_workers=min(8, len(srcs) + 1)) as ex:
         binding = ex.submit(_compile_binding, verbose)
         objs = list(ex.map(lambda s: _compile(s, verbose, list(extra)), srcs))
+        _link(objs, verbose, extra)
         binding_obj = binding.result()
-    if (not os.path.exists(LIB) or extra or
-            os.path.getmtime(LIB) < max(os.path.getmtime(o) for o in objs)):
-        tmp = LIB + ".tmp"
-        cmd = [nvcc(), *ARCH, "-shared", "-cudart", "static", "-o", tmp, *objs,
-               "-lrt", "-ldl", "-lpthread"]
-        if verbose:
-            print(" ".join(cmd), flush=True)
-        res = subprocess.run(cmd, capture_output=True, text=True)
-        if res.returncode != 0:
-            raise RuntimeError(f"link failed:\n{res.stdout}\n{res.stderr}")
-        os.replace(tmp, LIB)
     _link_binding(binding_obj, verbose)
     return LIB
 
