@@ -403,8 +403,9 @@ __device__ __forceinline__ long long part_row(const AttnParams& p, int i, int ct
 // 2^y for a pair of arguments, without the special-function unit: y = n + f with n
 // whole and |f| <= 1/2 (adding 1.5 * 2^23 leaves n in the low mantissa bits), 2^f by the
 // minimax polynomial of degree 4 (Remez exchange on [-1/2, 1/2]: relative error 2.65e-6 by its
-// coefficients, 2.8e-6 with the f32 steps), and n added to the exponent.  Results end at 2^-126 and 2^127; a NaN gives
-// 2^127, which no row's sum may hold, so its tile is done again without the polynomial.
+// coefficients, 2.8e-6 with the f32 steps), and n added to the exponent.  Results end at 2^-126
+// and 2^127; a NaN gives 2^127, which no row's sum may hold, so its tile is done again without
+// the polynomial.
 __device__ __forceinline__ float2 poly_exp2(float2 y) {
   const float2 magic = make_float2(12582912.f, 12582912.f), back = make_float2(-12582912.f, -12582912.f);
   y.x = fmaxf(fminf(y.x, 127.f), -126.f);
@@ -1715,8 +1716,8 @@ bool make_map_pool(CUtensorMap* map, const void* base, const nabla_cache& c) {
 // sequence fills at least half of an item by itself: over a short prefix the padding of its
 // 256 rows costs less than parts and their join.  Own against shared, us: 130 rows over 300,
 // 1000, 3000 tokens 38 : 45, 48 : 49, 73 : 66; 168 rows over 1000, 3000, 6000 79 : 109, 140 :
-// 154, 221 : 214; 200 rows over 3000, 12000 134 : 155, 367 : 374 (there the rule takes the second, 2%
-// slower).  The rule knows neither the number of sequences nor of key heads, on which the cost of
+// 154, 221 : 214; 200 rows over 3000, 12000 134 : 155, 367 : 374 (there the rule takes the
+// second, 2% slower).  The rule knows neither the number of sequences nor of key heads, on which the cost of
 // reading the prefix again and of joining parts depends.
 bool is_shared(long long R, long long P) {
   if (R < kRows / 2 || R >= kRows) return R < kRows;

@@ -14,8 +14,9 @@
 // token (two 16-byte vectors of a 16-bit tensor) and walks a group of heads with them, so
 // the fp64 angles and the sines are computed once for the whole group; it keeps the loads
 // of two heads in flight.  The angles come first, so calls of one or two waves (the appended
-// tokens above) show their latency; in larger ones other warps hide it.  Neighbouring threads own a token's neighbouring pairs and
-// then the neighbouring tokens, so a head's accesses are contiguous runs.
+// tokens above) show their latency; in larger ones other warps hide it.  Neighbouring threads
+// own a token's neighbouring pairs and then the neighbouring tokens, so a head's accesses are
+// contiguous runs.
 //
 // Half-split pairs (i, i + dim / 2) with dim / 2 no multiple of 8 have no common 16-byte
 // alignment of their parts: rotary_staged_kernel turns them in shared memory (97 MB of f32
@@ -390,12 +391,12 @@ cudaError_t go(RotaryParams p, cudaStream_t st) {
   const long long lanes = static_cast<long long>(p.tokens) * kLanes;
   // Heads per thread: as many as launch about 8 warps of threads for each of the GPU's 592
   // schedulers, so that the angles (about 3 us of latency) are shared by many heads; a small
-  // call spreads its heads over threads instead.  6 of them are resident with 80 registers
+  // call spreads its heads over threads instead.  6 of the 8 are resident with 80 registers
   // (16 bits, interleaved), 5 with 90 (half-split): calls of the rule's size end in a partly
-  // empty wave (3 x 4,097 tokens 1,538 blocks on 740 places, 7,168 appended ones 1,344 on 888).  Sequences [3, 4097] of 24 heads: 118 us at
-  // one head a thread, 33 us at four and more.  One sequence of 7,168 tokens, 48 heads: 37 us
-  // at 8 warps, 43 at 6 and at 4, 39 at 12.  Blocks of 128 threads and two heads in flight beat
-  // 256 and four (720p-like Q and K 499 against 507 us).
+  // empty wave (3 x 4,097 tokens 1,538 blocks on 740 places, 7,168 appended ones 1,344 on 888).
+  // Sequences [3, 4097] of 24 heads: 118 us at one head a thread, 33 us at four and more.  One
+  // sequence of 7,168 tokens, 48 heads: 37 us at 8 warps, 43 at 6 and at 4, 39 at 12.  Blocks of
+  // 128 threads and two heads in flight beat 256 and four (720p-like Q and K 499 against 507 us).
   long long g = lanes * p.heads / (148LL * 1024);
   g = g < 1 ? 1 : (g > p.heads ? p.heads : g);
   const int groups = static_cast<int>((p.heads + g - 1) / g);
