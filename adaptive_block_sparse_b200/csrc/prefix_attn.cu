@@ -360,7 +360,8 @@ struct Cfg {
 // A CTA's status word holds the largest rank of what its threads recorded.  (The reduction
 // itself: with atomicMax() ptxas loads 64 bytes more of spills in the long items' kernel.)
 __device__ __forceinline__ void record_rank(uint32_t* status, uint32_t code) {
-  asm volatile("red.global.max.u32 [%0], %1;" ::"l"(__cvta_generic_to_global(status)), "r"(status_rank(code)) : "memory");
+  asm volatile("red.global.max.u32 [%0], %1;" ::"l"(__cvta_generic_to_global(status)), "r"(status_rank(code))
+               : "memory");
 }
 
 // mbar_wait() for short hand-overs: probes without reading the timer, which is looked at (and

@@ -279,7 +279,7 @@ nabla_status nabla_selftest_bounded_wait(void *workspace, size_t workspace_bytes
 
 /* Reads (synchronously on `stream`) the device status word that the kernels of the
  * last call on `workspace` recorded: 0 = fine, otherwise a code naming the barrier
- * wait that gave up.  Returns NABLA_ERR_DEVICE_CHECK when the word is non-zero, and
+ * wait that gave up or the error found in the inputs.  Returns NABLA_ERR_DEVICE_CHECK when the word is non-zero, and
  * clears it.  `code` (nullable) receives the raw word. */
 nabla_status nabla_read_device_status(void *workspace, uint32_t *code,
                                       nabla_stream_t stream);

@@ -220,6 +220,17 @@ def test_repeated_calls_give_the_same_bits(name):
         assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
 
 
+@pytest.mark.parametrize("name", ["token", "drafted", "causal into the prefix"])
+def test_a_wider_page_table_cuts_the_work_another_way(name):
+    """Small calls of few rows take a CTA for every tile that the table can hold, wider ones runs: other
+    parts, the same result within the tolerance, and each width repeats its own bits."""
+    for extra in (0, 2000):
+        pr = Problem(**{**CASES[name], "width_extra": extra}, seed=18)
+        a, b = pr.run(), pr.run()
+        pr.check(*a)
+        assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
 @pytest.mark.parametrize("dtype", [BF, F16])
 def test_peaked_and_large_scores(dtype):
     """Maxima that grow along the keys, by far more than one rescale's step, and rows that one key
